@@ -2,14 +2,18 @@
 
 The product is the C-ABI library ``libgdn_decode.so`` (declared in
 ``include/gdn_decode.h``), whose sm_100a kernel performs the whole decode /
-speculative-decode state update.  ``binding`` is a thin ctypes layer that
-marshals torch tensors into that ABI; ``workloads`` draws seeded synthetic
-inputs.  The binding loads the library on first use and raises if it is
-missing: there is no CPU or library fallback.
+speculative-decode state update, and beside it ``libgdn_spec.so``
+(``include/gdn_spec.h``) with the other operators of a speculative step:
+index arrays, probabilities, verification of drafts, commit of states.
+``binding`` and ``speculative`` are thin ctypes layers that marshal torch
+tensors into those ABIs; ``workloads`` draws seeded synthetic inputs.  The
+bindings load their library on first use and raise if it is missing: there is
+no CPU or library fallback.
 """
 from __future__ import annotations
 
-__all__ = ["decode_update", "recurrent_update", "gating", "binding", "workloads"]
+__all__ = ["decode_update", "recurrent_update", "gating", "token_probs", "verify_drafts", "commit_states",
+           "step_maps", "binding", "speculative", "workloads"]
 
 
 def __getattr__(name):
@@ -20,7 +24,11 @@ def __getattr__(name):
                 "CHECK_INDICES", "LAUNCH_PDL"):
         from . import binding
         return getattr(binding, name)
-    if name in ("binding", "workloads", "build"):
+    if name in ("token_probs", "verify_drafts", "commit_states", "step_maps", "PreparedTokenProbs",
+                "PreparedVerifyDrafts", "PreparedCommitStates", "PreparedStepMaps"):
+        from . import speculative
+        return getattr(speculative, name)
+    if name in ("binding", "speculative", "workloads", "build"):
         import importlib
         return importlib.import_module(f"{__name__}.{name}")
     raise AttributeError(name)

@@ -1,0 +1,111 @@
+// gdn_spec_common.cuh -- device helpers of the speculative-step kernels:
+// thread-block clusters, distributed shared memory, element conversions.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "gdn_spec.h"
+#include "mbarrier_sm100.cuh"
+
+namespace gdn {
+namespace spec {
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ void report(uint32_t *status, uint32_t bits)
+{
+    if (status)
+        atomicOr(status, bits);
+}
+
+// ---- clusters.  Every thread of every CTA takes part in each barrier.
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// Address of this CTA's shared variable `p` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(sync::smem_addr(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_peer(uint32_t addr, float x, float y)
+{
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void st_peer(uint32_t addr, double x)
+{
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(x) : "memory");
+}
+
+// ---- elements
+template <typename T> struct Elem;
+template <> struct Elem<float> {
+    static constexpr int PER16 = 4;
+    __device__ static float get(float x) { return x; }
+    __device__ static float put(float x) { return x; }
+};
+template <> struct Elem<__nv_bfloat16> {
+    static constexpr int PER16 = 8;
+    __device__ static float get(__nv_bfloat16 x) { return __bfloat162float(x); }
+    __device__ static __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
+};
+
+// The values of a 16-byte word.
+__device__ __forceinline__ void unpack16(const uint4 &w, float (&x)[4], const float *)
+{
+    x[0] = __uint_as_float(w.x);
+    x[1] = __uint_as_float(w.y);
+    x[2] = __uint_as_float(w.z);
+    x[3] = __uint_as_float(w.w);
+}
+__device__ __forceinline__ void unpack16(const uint4 &w, float (&x)[8], const __nv_bfloat16 *)
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+
+// 2^x, relative error about 2^-22; -inf gives 0.
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The packed rows of sequence i: false (and a status bit) when cu_seqlens are
+// not usable for it.
+__device__ __forceinline__ bool rows_of(const int32_t *cu, int32_t T_fixed, int32_t T_tot, int32_t i, int32_t *start,
+                                        int32_t *len)
+{
+    if (!cu) {
+        *start = i * T_fixed;
+        *len = T_fixed;
+        return true;
+    }
+    const int32_t a = cu[i], b = cu[i + 1];
+    *start = a;
+    *len = b - a;
+    return a >= 0 && b >= a && b <= T_tot;
+}
+
+}  // namespace spec
+}  // namespace gdn
