@@ -106,8 +106,8 @@ cudaError_t launch_cluster(Kernel kernel, int64_t ctas, int cluster, int threads
 int status_from(cudaError_t err) { return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
 
 template <typename TIn, typename TOut>
-cudaError_t launch_probs(const gdn::spec::ProbsParams &p, int64_t rows, int cluster, size_t smem, cudaStream_t stream,
-                         bool pdl)
+cudaError_t launch_probs(const gdn::spec::ProbsParams &p, int64_t rows, int cluster, int threads, size_t smem,
+                         cudaStream_t stream, bool pdl)
 {
     static PerDevice once;
     int dev = 0;
@@ -120,19 +120,37 @@ cudaError_t launch_probs(const gdn::spec::ProbsParams &p, int64_t rows, int clus
         });
     if (err != cudaSuccess)
         return err;
-    return launch_cluster(gdn::spec::gdn_token_probs_kernel<TIn, TOut>, rows * cluster, cluster,
-                          gdn::spec::PROBS_THREADS, smem, stream, pdl, p);
+    return launch_cluster(gdn::spec::gdn_token_probs_kernel<TIn, TOut>, rows * cluster, cluster, threads, smem, stream, pdl, p);
 }
 
-// CTAs per row or sequence: enough that no slice is longer than `most`
-// elements, then more (up to 8) while the grid leaves SMs idle and a slice
-// keeps `least` elements.
-int cluster_for(int64_t units, int64_t vocab, int64_t most, int64_t least, int sms)
+// CTAs per row of token probabilities: slices of at most 16384 elements, and
+// more CTAs (up to 8) while the grid leaves SMs idle and a slice keeps 1024.
+int probs_cluster(int64_t rows, int64_t vocab, int sms)
 {
     int c = 1;
-    while (c < 8 && (vocab > c * most || (units * c < sms && vocab > c * least)))
+    while (c < 8 && (vocab > c * 16384ll || (rows * c < sms && vocab > c * 1024ll)))
         c *= 2;
     return c;
+}
+
+// CTAs per sequence of a verification: as many (up to 8) as stay resident at
+// once, four of 256 threads an SM, while a CTA keeps 1024 elements.
+int verify_cluster(int64_t sequences, int64_t vocab, int sms)
+{
+    int c = 1;
+    while (c < 8 && sequences * c * 2 <= 4ll * sms && vocab > c * 1024ll)
+        c *= 2;
+    return c;
+}
+
+// Threads of a CTA that has `words` 16-byte words of work: 256, or as many as
+// there are words (up to 1024) when the CTAs have an SM each.
+int threads_for(int64_t ctas, int64_t words, int sms)
+{
+    int t = 256;
+    while (ctas <= sms && t < 1024 && words > t)
+        t *= 2;
+    return t;
 }
 
 }  // namespace
@@ -193,17 +211,18 @@ GDN_API int gdn_token_probs(const gdn_tensor *logits, const gdn_tensor *temperat
     p.t_stride = temperature ? temperature->stride[0] : 0;
     p.vocab = static_cast<int32_t>(vocab);
     p.num_temps = temperature ? static_cast<int32_t>(temperature->shape[0]) : 0;
-    const int cluster = cluster_for(R, vocab, 16384, 1024, sms);
+    const int cluster = probs_cluster(R, vocab, sms);
     p.slice = static_cast<int32_t>(((vocab + cluster - 1) / cluster + 7) / 8 * 8);
+    const int threads = threads_for(R * cluster, p.slice / 8, sms);
     const size_t smem = gdn::spec::probs_smem(p.slice * elem_size(logits->dtype));
     const cudaStream_t stream = stream_of(extra);
     const bool pdl = (flags & GDN_LAUNCH_PDL) != 0;
     const bool in16 = logits->dtype == GDN_DTYPE_BF16, out16 = probs->dtype == GDN_DTYPE_BF16;
     using bf16 = __nv_bfloat16;
-    return status_from(in16 ? (out16 ? launch_probs<bf16, bf16>(p, R, cluster, smem, stream, pdl)
-                                     : launch_probs<bf16, float>(p, R, cluster, smem, stream, pdl))
-                            : (out16 ? launch_probs<float, bf16>(p, R, cluster, smem, stream, pdl)
-                                     : launch_probs<float, float>(p, R, cluster, smem, stream, pdl)));
+    return status_from(in16 ? (out16 ? launch_probs<bf16, bf16>(p, R, cluster, threads, smem, stream, pdl)
+                                     : launch_probs<bf16, float>(p, R, cluster, threads, smem, stream, pdl))
+                            : (out16 ? launch_probs<float, bf16>(p, R, cluster, threads, smem, stream, pdl)
+                                     : launch_probs<float, float>(p, R, cluster, threads, smem, stream, pdl)));
 }
 
 GDN_API int gdn_verify_drafts(const gdn_tensor *target_probs, const gdn_tensor *draft_tokens,
@@ -285,16 +304,17 @@ GDN_API int gdn_verify_drafts(const gdn_tensor *target_probs, const gdn_tensor *
     p.T_fixed = varlen ? 0 : static_cast<int32_t>(L.T);
     p.T_tot = static_cast<int32_t>(L.T_tot);
     p.vocab = static_cast<int32_t>(vocab);
-    const int cluster = cluster_for(N, vocab, 8192, 1024, sms);
-    const int64_t segs = static_cast<int64_t>(cluster) * gdn::spec::VERIFY_WARPS;
+    const int cluster = verify_cluster(N, vocab, sms);
+    const int threads = threads_for(N * cluster, vocab / cluster / 8, sms);
+    const int64_t segs = static_cast<int64_t>(cluster) * (threads / 32);
     p.seg = static_cast<int32_t>(((vocab + segs - 1) / segs + 31) / 32 * 32);
     const cudaStream_t stream = stream_of(extra);
     const bool pdl = (flags & GDN_LAUNCH_PDL) != 0;
     return status_from(target_probs->dtype == GDN_DTYPE_BF16
                            ? launch_cluster(gdn::spec::gdn_verify_drafts_kernel<__nv_bfloat16>, N * cluster, cluster,
-                                            gdn::spec::VERIFY_THREADS, 0, stream, pdl, p)
+                                            threads, 0, stream, pdl, p)
                            : launch_cluster(gdn::spec::gdn_verify_drafts_kernel<float>, N * cluster, cluster,
-                                            gdn::spec::VERIFY_THREADS, 0, stream, pdl, p));
+                                            threads, 0, stream, pdl, p));
 }
 
 GDN_API int gdn_commit_states(const gdn_tensor *intermediate_states, const gdn_tensor *num_tokens,

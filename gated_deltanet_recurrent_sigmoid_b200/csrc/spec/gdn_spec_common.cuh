@@ -43,9 +43,9 @@ __device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(sync::smem_addr(p)), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void st_peer(uint32_t addr, float x, float y)
+__device__ __forceinline__ void st_peer(uint32_t addr, float x)
 {
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
 }
 __device__ __forceinline__ void st_peer(uint32_t addr, double x)
 {
@@ -81,6 +81,43 @@ __device__ __forceinline__ void unpack16(const uint4 &w, float (&x)[8], const __
         x[2 * i] = __uint_as_float(u[i] << 16);
         x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
+}
+
+// The largest value of a 16-byte word; NaN is passed over (all NaN: NaN).
+__device__ __forceinline__ float max16(const uint4 &w, const float *)
+{
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+__device__ __forceinline__ float max16(const uint4 &w, const __nv_bfloat16 *)
+{
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&w);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
+// N consecutive elements of shared memory at an address aligned to
+// min(16, their size) bytes.
+__device__ __forceinline__ void load_group(const float *p, float (&x)[4])
+{
+    unpack16(*reinterpret_cast<const uint4 *>(p), x, static_cast<const float *>(nullptr));
+}
+__device__ __forceinline__ void load_group(const float *p, float (&x)[8])
+{
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load_group(const __nv_bfloat16 *p, float (&x)[8])
+{
+    unpack16(*reinterpret_cast<const uint4 *>(p), x, static_cast<const __nv_bfloat16 *>(nullptr));
+}
+__device__ __forceinline__ void load_group(const __nv_bfloat16 *p, float (&x)[4])
+{
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    x[0] = __uint_as_float(w.x << 16);
+    x[1] = __uint_as_float(w.x & 0xffff0000u);
+    x[2] = __uint_as_float(w.y << 16);
+    x[3] = __uint_as_float(w.y & 0xffff0000u);
 }
 
 // 2^x, relative error about 2^-22; -inf gives 0.

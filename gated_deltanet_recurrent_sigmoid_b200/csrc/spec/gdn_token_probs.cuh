@@ -3,11 +3,10 @@
 //
 // p_v = exp((l_v - m) / t) / sum_w exp((l_w - m) / t), m the row's maximum.
 // One cluster per row; each CTA holds a contiguous slice of the row in shared
-// memory (one bulk copy per piece, so HBM is read once), and the row's
-// maximum and sum come from one pass that keeps both running:
-//     (m, s) + x  ->  (m', s 2^((m - m') c) + 2^((x - m') c)),  c = log2(e) / t.
-// The CTAs' pairs cross the cluster through distributed shared memory, one
-// barrier, and the second pass reads the slice again from shared memory.
+// memory (bulk copies, so HBM is read once) and passes over it three times:
+// maximum (as the pieces come in), sum of 2^((l - m) c) with c = log2(e) / t,
+// and the probabilities, whose powers are taken again rather than kept.  Each
+// of the first two ends in one exchange over distributed shared memory.
 // Bound by HBM: each logit read once, each probability written once.
 #pragma once
 
@@ -28,15 +27,15 @@ struct ProbsParams {
     int32_t num_temps;
 };
 
-constexpr int PROBS_THREADS = 256;
+constexpr int PROBS_MAX_THREADS = 1024;
 constexpr int PROBS_PIECE = 8192;                          // bytes per bulk copy and mbarrier
 constexpr int PROBS_MAX_SLICE_BYTES = GDN_SPEC_MAX_VOCAB / 8 * 4;
 constexpr int PROBS_MAX_PIECES = PROBS_MAX_SLICE_BYTES / PROBS_PIECE + 2;
 constexpr int PROBS_MAX_CLUSTER = 8;
 
 struct ProbsShared {
-    float2 cta[PROBS_MAX_CLUSTER];                         // (m, s) or (m, index) of each CTA of the cluster
-    float2 warp[PROBS_THREADS / 32];
+    float cta[3][PROBS_MAX_CLUSTER];                       // one value of each CTA of the cluster, per reduction
+    float warp[PROBS_MAX_THREADS / 32];
     unsigned long long full[PROBS_MAX_PIECES];
     int failed;
     alignas(16) unsigned char raw[1];                      // the slice, at its global address modulo 16
@@ -45,32 +44,59 @@ struct ProbsShared {
 // Bytes of dynamic shared memory for a slice of `bytes`.
 inline size_t probs_smem(int64_t bytes) { return offsetof(ProbsShared, raw) + static_cast<size_t>(bytes) + 32; }
 
-// (m, s) joined with (m2, s2); empty sides have m = -inf, s = 0.
-__device__ __forceinline__ void join(float &m, float &s, float m2, float s2, float c)
+struct Max {
+    static constexpr float EMPTY = -INFINITY;
+    __device__ static float of(float a, float b) { return fmaxf(a, b); }
+};
+struct Sum {
+    static constexpr float EMPTY = 0.f;
+    __device__ static float of(float a, float b) { return a + b; }
+};
+
+// Over all threads of the cluster, the same bits in each of them (the order is
+// fixed).  `slot`: which of sh.cta, not used again in the kernel.
+template <typename Op>
+__device__ __forceinline__ float over_cluster(float x, ProbsShared &sh, int slot, uint32_t rank, uint32_t size)
 {
-    const float top = fmaxf(m, m2);
-    const float f = m == top ? 1.f : ex2((m - top) * c), f2 = m2 == top ? 1.f : ex2((m2 - top) * c);
-    s = s * f + s2 * f2;
-    m = top;
+    const int tid = threadIdx.x, lane = tid & 31;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        x = Op::of(x, __shfl_xor_sync(~0u, x, o));
+    if (lane == 0)
+        sh.warp[tid >> 5] = x;
+    __syncthreads();
+    if (tid < 32) {
+        x = lane < static_cast<int>(blockDim.x >> 5) ? sh.warp[lane] : Op::EMPTY;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            x = Op::of(x, __shfl_xor_sync(~0u, x, o));
+        if (lane < static_cast<int>(size))
+            st_peer(peer_addr(&sh.cta[slot][rank], lane), x);
+    }
+    cluster_arrive();
+    cluster_wait();
+    x = sh.cta[slot][0];
+    for (uint32_t i = 1; i < size; ++i)
+        x = Op::of(x, sh.cta[slot][i]);
+    return x;
 }
 
-// The larger value, the lower index of equals; an empty side has v = -inf and
-// index INT32_MAX.
-__device__ __forceinline__ void first_max(float &v, int32_t &i, float v2, int32_t i2)
-{
-    if (v2 > v || (v2 == v && i2 < i)) {
-        v = v2;
-        i = i2;
-    }
-}
+// 2^((x - m) c) up to a factor that is the same for the whole row.  fast:
+// one fused multiply-add, x c - (m c), the rounding of m c being that factor;
+// careful: any maximum and temperature, NaN as 0.
+struct Power {
+    float c, top, mc;
+    __device__ float fast(float x) const { return ex2(fmaf(x, c, -mc)); }
+    __device__ float careful(float x) const { return x == top ? 1.f : (x == x ? ex2((x - top) * c) : 0.f); }
+};
 
 template <typename TIn, typename TOut>
-__global__ void __launch_bounds__(PROBS_THREADS) gdn_token_probs_kernel(const ProbsParams p)
+__global__ void __launch_bounds__(PROBS_MAX_THREADS) gdn_token_probs_kernel(const ProbsParams p)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     ProbsShared &sh = *reinterpret_cast<ProbsShared *>(smem);
     constexpr int PI = Elem<TIn>::PER16, PO = Elem<TOut>::PER16;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, threads = blockDim.x;
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int64_t row = blockIdx.x / size;
 
@@ -94,15 +120,15 @@ __global__ void __launch_bounds__(PROBS_THREADS) gdn_token_probs_kernel(const Pr
     }
 
     // ---- the slice into shared memory: the 16-byte words inside it by bulk
-    // copies, the ragged edges by plain loads
+    // copies, the ragged edges (fewer than 16 bytes on either side) by plain
+    // loads, one element a thread
     const int32_t e0 = min(p.vocab, static_cast<int32_t>(rank) * p.slice);
     const int32_t n = min(p.vocab - e0, p.slice);
     const TIn *src = static_cast<const TIn *>(p.logits) + row * p.l_row + e0;
     const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) & 15u);
     const uint32_t bytes = static_cast<uint32_t>(n) * sizeof(TIn);
-    const uint32_t b0 = off ? 16u : 0u, b1 = (off + bytes) & ~15u;   // words inside, offsets in raw
-    const uint32_t bulk = b1 > b0 ? b1 - b0 : 0u;
-    const int pieces = static_cast<int>((bulk + PROBS_PIECE - 1) / PROBS_PIECE);
+    const uint32_t b0 = off ? 16u : 0u, b1 = max(b0, (off + bytes) & ~15u);   // the words, as offsets in raw
+    const int pieces = static_cast<int>((b1 - b0 + PROBS_PIECE - 1) / PROBS_PIECE);
     if (tid == 0) {
         sh.failed = 0;
         for (int i = 0; i < pieces; ++i)
@@ -117,141 +143,134 @@ __global__ void __launch_bounds__(PROBS_THREADS) gdn_token_probs_kernel(const Pr
         }
     }
     TIn *const el = reinterpret_cast<TIn *>(sh.raw + off);           // el[0 .. n)
-    {
-        const int32_t head = bulk ? static_cast<int32_t>((b0 - off) / sizeof(TIn)) : n;   // elements before the words
-        const int32_t tail = bulk ? static_cast<int32_t>((b1 - off) / sizeof(TIn)) : n;   // first one behind them
-        if (tid < head)
-            el[tid] = src[tid];
-        if (tail + tid < n)
-            el[tail + tid] = src[tail + tid];
+    const int32_t head = b1 > b0 ? static_cast<int32_t>((b0 - off) / sizeof(TIn)) : n;   // elements before the words
+    const int32_t tail = b1 > b0 ? static_cast<int32_t>((b1 - off) / sizeof(TIn)) : n;   // the first behind them
+    const int32_t edge = tid < head ? tid : tail + tid - head;       // this thread's ragged element, if < n
+    const bool has_edge = edge < n;
+    float edge_x = -INFINITY;
+    if (has_edge) {
+        const TIn x = src[edge];
+        el[edge] = x;
+        edge_x = Elem<TIn>::get(x);
     }
     const float t = p.temperature ? p.temperature[ti * p.t_stride] : 1.f;
     const bool bad = !(t >= 0.f) || isinf(t), greedy = t == 0.f;
-    // log2(e) / t, at most about 1e38 so that 0 * c is 0
+    // log2(e) / t, at most 1e38 so that 0 * c is 0
     const float c = greedy || bad ? 0.f : fminf(static_cast<float>(1.4426950408889634 / static_cast<double>(t)), 1e38f);
     if (bad && rank == 0 && tid == 0)
         report(p.status, GDN_DEV_BAD_TEMPERATURE);
     __syncthreads();
 
-    // ---- pass 1: the running (maximum, sum), or (maximum, its first index)
-    float m = -INFINITY, s = 0.f;
-    int32_t at_max = INT32_MAX;
-    const int words = static_cast<int>((off + bytes + 15u) >> 4);
+    // ---- the maximum (NaN is no operand of it), as the pieces come in
+    const uint4 *const words = reinterpret_cast<const uint4 *>(sh.raw + b0);
+    const int num_words = static_cast<int>((b1 - b0) / 16u);
+    float top = edge_x;
     bool ok = true;
-    int have = 0;                                          // pieces known to be in
-    for (int w = tid; w < words && ok; w += PROBS_THREADS) {
-        const uint32_t b = static_cast<uint32_t>(w) * 16u;
-        if (b >= b0 && b < b1) {
-            const int piece = static_cast<int>((b - b0) / PROBS_PIECE);
-            while (ok && have <= piece)
-                ok = sync::mbar_wait(&sh.full[have++], 0, &sh.failed);
-            if (!ok)
-                break;
-        }
-        float x[PI];
-        unpack16(*reinterpret_cast<const uint4 *>(sh.raw + b), x, static_cast<const TIn *>(nullptr));
-        const int32_t first = static_cast<int32_t>(b / sizeof(TIn)) - static_cast<int32_t>(off / sizeof(TIn));
-        float top = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < PI; ++j) {
-            if (first + j < 0 || first + j >= n || !(x[j] == x[j]))
-                x[j] = -INFINITY;                          // outside the slice, or NaN
-            top = fmaxf(top, x[j]);
-        }
-        if (top == -INFINITY)
-            continue;
-        if (greedy) {
-#pragma unroll
-            for (int j = PI - 1; j >= 0; --j)
-                if (x[j] == top && (top > m || (top == m && first + j < at_max)))
-                    at_max = first + j, m = top;
-        } else {
-            const float to = fmaxf(m, top);
-            float sum = m == to ? s : s * ex2((m - to) * c);
-#pragma unroll
-            for (int j = 0; j < PI; ++j)
-                sum += x[j] == to ? 1.f : ex2((x[j] - to) * c);
-            m = to;
-            s = sum;
-        }
+    for (int k = 0; k < pieces && ok; ++k) {
+        ok = sync::mbar_wait(&sh.full[k], 0, &sh.failed);
+        if (!ok)
+            break;
+        const int w1 = min(num_words, (k + 1) * (PROBS_PIECE / 16));
+        for (int w = k * (PROBS_PIECE / 16) + tid; w < w1; w += threads)
+            top = fmaxf(top, max16(words[w], static_cast<const TIn *>(nullptr)));
     }
     if (!ok) {
         sh.failed = 1;
         report(p.status, GDN_DEV_TIMEOUT);
     }
-    if (greedy && at_max != INT32_MAX)
-        at_max += e0;
+    cluster_wait();
+    top = over_cluster<Max>(top, sh, 0, rank, size);
 
-    // ---- over the warp, the CTA and the cluster.  For a greedy row the second
-    // member carries the index's bits.
+    // ---- the sum of the powers, or the first index of the maximum.  The fast
+    // form needs m c within 2^20, where its rounding is far below 1.
+    const Power power = {c, top, top * c};
+    bool fast = !greedy && !bad && fabsf(power.mc) < 1048576.f;
+    const bool zeros = bad || top == -INFINITY;
+    float inv = 0.f;
+    int32_t pick = -1;
+    if (greedy) {
+        int32_t first = INT32_MAX;
+        if (!zeros)
+            for (int32_t j = tid; j < n; j += threads)
+                if (Elem<TIn>::get(el[j]) == top) {
+                    first = j;
+                    break;
+                }
+        // indices below 2^24 are exact in fp32
+        const float g = over_cluster<Max>(first == INT32_MAX ? -INFINITY : -static_cast<float>(e0 + first), sh, 1, rank, size);
+        pick = zeros ? -1 : static_cast<int32_t>(-g) - e0;
+    } else if (!zeros) {
+        if (fast) {
+            float s0 = has_edge ? power.fast(edge_x) : 0.f, s1 = 0.f;
+            for (int w = tid; w < num_words; w += threads) {
+                float x[PI];
+                unpack16(words[w], x, static_cast<const TIn *>(nullptr));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(~0u, m, o), s2 = __shfl_xor_sync(~0u, s, o);
-        const int32_t i2 = __shfl_xor_sync(~0u, at_max, o);
-        if (greedy)
-            first_max(m, at_max, m2, i2);
-        else
-            join(m, s, m2, s2, c);
-    }
-    if (lane == 0)
-        sh.warp[warp] = make_float2(m, greedy ? __int_as_float(at_max) : s);
-    __syncthreads();
-    cluster_wait();
-    if (tid < static_cast<int>(size)) {
-        float2 a = sh.warp[0];
-        int32_t ai = __float_as_int(a.y);
-        for (int i = 1; i < PROBS_THREADS / 32; ++i) {
-            const float2 b = sh.warp[i];
-            if (greedy)
-                first_max(a.x, ai, b.x, __float_as_int(b.y));
-            else
-                join(a.x, a.y, b.x, b.y, c);
+                for (int j = 0; j < PI; j += 2) {
+                    s0 += power.fast(x[j]);
+                    s1 += power.fast(x[j + 1]);
+                }
+            }
+            const float s = over_cluster<Sum>(s0 + s1, sh, 1, rank, size);
+            fast = s == s;                                 // a NaN logit: again, without it
+            inv = 1.f / s;
         }
-        st_peer(peer_addr(&sh.cta[rank], tid), a.x, greedy ? __int_as_float(ai) : a.y);
-    }
-    cluster_arrive();
-    cluster_wait();
-    float2 all = sh.cta[0];
-    int32_t pick = __float_as_int(all.y);
-    for (uint32_t i = 1; i < size; ++i) {
-        const float2 b = sh.cta[i];
-        if (greedy)
-            first_max(all.x, pick, b.x, __float_as_int(b.y));
-        else
-            join(all.x, all.y, b.x, b.y, c);
+        if (!fast) {
+            float s = 0.f;
+            for (int32_t j = tid; j < n; j += threads)
+                s += power.careful(Elem<TIn>::get(el[j]));
+            inv = 1.f / over_cluster<Sum>(s, sh, 2, rank, size);
+        }
     }
     pdl_trigger();
-    const float top = all.x;
-    const float inv = top == -INFINITY || bad ? 0.f : 1.f / all.y;   // masked rows: zeros
 
-    // ---- pass 2: the probabilities, 16 bytes at a time where they are aligned
+    // ---- the probabilities, 16 bytes at a time
     if (!sh.failed) {
-        TOut *dst = static_cast<TOut *>(p.probs) + row * p.p_row + e0;
-        const int32_t o_off = static_cast<int32_t>((reinterpret_cast<uintptr_t>(dst) & 15u) / sizeof(TOut));
-        const int groups = (o_off + n + PO - 1) / PO;
-        auto value = [&](int32_t j) -> float {
-            if (greedy)
-                return top > -INFINITY && e0 + j == pick ? 1.f : 0.f;
-            const float x = Elem<TIn>::get(el[j]);
-            const float e = x == top ? 1.f : ex2((x - top) * c);
-            return x == x && inv > 0.f ? e * inv : 0.f;
-        };
-        for (int g = tid; g < groups; g += PROBS_THREADS) {
-            const int32_t j0 = g * PO - o_off;
-            if (j0 >= 0 && j0 + PO <= n) {
+        TOut *const dst = static_cast<TOut *>(p.probs) + row * p.p_row + e0;
+        const int32_t skew = static_cast<int32_t>((reinterpret_cast<uintptr_t>(dst) & 15u) / sizeof(TOut));
+        const int32_t first = min(n, skew ? PO - skew : 0);          // elements before the first 16-byte group
+        const int groups = (n - first) / PO;
+        const int32_t rest = first + groups * PO;                    // elements behind the last
+        auto write = [&](auto value) {
+            const int32_t lone = tid < first ? tid : rest + tid - first;
+            if (lone < n)
+                dst[lone] = Elem<TOut>::put(value(lone, Elem<TIn>::get(el[lone])));
+            const TIn *const from = el + first;
+            uint4 *const to = reinterpret_cast<uint4 *>(dst + first);
+            auto store = [&](int g, const float (&x)[PO]) {
                 alignas(16) TOut v[PO];
 #pragma unroll
                 for (int j = 0; j < PO; ++j)
-                    v[j] = Elem<TOut>::put(value(j0 + j));
-                *reinterpret_cast<uint4 *>(dst + j0) = *reinterpret_cast<const uint4 *>(v);
+                    v[j] = Elem<TOut>::put(value(first + g * PO + j, x[j]));
+                to[g] = *reinterpret_cast<const uint4 *>(v);
+            };
+            constexpr int GROUP_BYTES = PO * sizeof(TIn);            // 8, 16 or 32
+            if (sync::smem_addr(from) % (GROUP_BYTES < 16 ? GROUP_BYTES : 16) == 0) {
+#pragma unroll 2
+                for (int g = tid; g < groups; g += threads) {
+                    float x[PO];
+                    load_group(from + g * PO, x);
+                    store(g, x);
+                }
             } else {
-                for (int32_t j = max(j0, 0); j < min(j0 + PO, n); ++j)
-                    dst[j] = Elem<TOut>::put(value(j));
+                for (int g = tid; g < groups; g += threads) {
+                    float x[PO];
+#pragma unroll
+                    for (int j = 0; j < PO; ++j)
+                        x[j] = Elem<TIn>::get(from[g * PO + j]);
+                    store(g, x);
+                }
             }
-        }
+        };
+        if (zeros || greedy)
+            write([&](int32_t j, float) { return j == pick ? 1.f : 0.f; });
+        else if (fast)
+            write([&](int32_t, float x) { return power.fast(x) * inv; });
+        else
+            write([&](int32_t, float x) { return power.careful(x) * inv; });
     } else {
         // copies still in flight must land before the CTA's memory goes
-        for (int i = tid; i < pieces; i += PROBS_THREADS) {
+        for (int i = tid; i < pieces; i += threads) {
             int never = 0;
             sync::mbar_wait(&sh.full[i], 0, &never);
         }

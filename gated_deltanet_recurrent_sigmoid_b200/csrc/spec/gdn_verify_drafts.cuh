@@ -33,36 +33,71 @@ struct VerifyParams {
     int32_t seg;                     // elements per warp
 };
 
-constexpr int VERIFY_THREADS = 256;
-constexpr int VERIFY_WARPS = VERIFY_THREADS / 32;
+constexpr int VERIFY_MAX_THREADS = 1024;
+constexpr int VERIFY_MAX_WARPS = VERIFY_MAX_THREADS / 32;
 constexpr int VERIFY_MAX_CLUSTER = 8;
-constexpr int VERIFY_MAX_SEGS = VERIFY_WARPS * VERIFY_MAX_CLUSTER;
-static_assert(VERIFY_MAX_SEGS == 64, "two segment sums a lane");
+constexpr int VERIFY_MAX_SEGS = VERIFY_MAX_WARPS * VERIFY_MAX_CLUSTER;
 
 // What the drafted distribution takes off p.
 enum class Less { none, row, token };
 
-// The weight of one token.  p > q and the finiteness tests are exact in fp32.
-__device__ __forceinline__ double weight(float p, float q)
+// The weight of one token: p - q (q = 0 without ROW) where that is positive
+// and both are finite.  Those tests are exact in fp32, the difference is taken
+// in fp64.
+template <bool ROW>
+__device__ __forceinline__ double weight(float p, float q, bool counts)
 {
-    return p > q && fabsf(p) < INFINITY && fabsf(q) < INFINITY ? static_cast<double>(p) - static_cast<double>(q) : 0.0;
+    if (ROW) {
+        counts = counts && p > q && p < INFINITY && q > -INFINITY;
+        return static_cast<double>(counts ? p : 0.f) - static_cast<double>(counts ? q : 0.f);
+    }
+    return static_cast<double>(counts && p > 0.f && p < INFINITY ? p : 0.f);
+}
+
+// A row's weights: p, less the row q or less the token `out`.
+template <typename T>
+struct Weights {
+    const T *p, *q;
+    int32_t out;
+    template <bool ROW>
+    __device__ __forceinline__ double at(int64_t v) const
+    {
+        return weight<ROW>(Elem<T>::get(p[v]), ROW ? Elem<T>::get(q[v]) : 0.f, v != out);
+    }
+};
+
+// Sum over v0 <= v < v1, this lane's share of it: every 32nd.
+template <bool ROW, typename T>
+__device__ __forceinline__ double lane_sum(const Weights<T> &w, int64_t v0, int64_t v1)
+{
+    constexpr int U = 16;                            // loads in flight a thread, of either row
+    const int lane = threadIdx.x & 31;
+    double s[4] = {0, 0, 0, 0};
+    int64_t v = v0 + lane;
+    for (; v + 32 * (U - 1) < v1; v += 32 * U) {
+        T p[U], q[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            p[k] = w.p[v + 32 * k];
+            if (ROW)
+                q[k] = w.q[v + 32 * k];
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            s[k & 3] += weight<ROW>(Elem<T>::get(p[k]), ROW ? Elem<T>::get(q[k]) : 0.f, v + 32 * k != w.out);
+    }
+    for (; v < v1; v += 32)
+        s[0] += w.template at<ROW>(v);
+    return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 template <typename T>
-__device__ __forceinline__ double weight_at(const T *p, const T *q, Less less, int32_t token, int32_t v)
-{
-    const float pv = Elem<T>::get(p[v]);
-    const float qv = less == Less::row ? Elem<T>::get(q[v]) : 0.f;
-    return less == Less::token && v == token ? 0.0 : weight(pv, qv);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(VERIFY_THREADS) gdn_verify_drafts_kernel(const VerifyParams a)
+__global__ void __launch_bounds__(VERIFY_MAX_THREADS) gdn_verify_drafts_kernel(const VerifyParams a)
 {
     __shared__ double part[2][VERIFY_MAX_SEGS];      // segment sums of the cluster, for either attempt
-    __shared__ double scan[VERIFY_WARPS];
+    __shared__ double scan[VERIFY_MAX_WARPS];
     __shared__ int first_over, last_positive;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int32_t i = static_cast<int32_t>(blockIdx.x / size);
 
@@ -80,7 +115,7 @@ __global__ void __launch_bounds__(VERIFY_THREADS) gdn_verify_drafts_kernel(const
     int32_t *const out = a.out + i * a.o_seq;
     if (!runs) {
         if (rank == 0) {
-            for (int j = tid; j <= a.D; j += VERIFY_THREADS)
+            for (int j = tid; j <= a.D; j += threads)
                 out[j * a.o_pos] = -1;
             if (tid == 0)
                 a.num[i * a.n_seq] = 0;
@@ -125,7 +160,7 @@ __global__ void __launch_bounds__(VERIFY_THREADS) gdn_verify_drafts_kernel(const
         }
     }
     if (rank == 0) {
-        for (int j = tid; j <= a.D; j += VERIFY_THREADS)
+        for (int j = tid; j <= a.D; j += threads)
             if (j != A)
                 out[j * a.o_pos] = j < A ? tokens[j * a.x_pos] : -1;
         if (tid == 0)
@@ -133,33 +168,31 @@ __global__ void __launch_bounds__(VERIFY_THREADS) gdn_verify_drafts_kernel(const
     }
 
     // ---- the sum of each segment
-    const T *const prow = target + A * a.t_row;
-    const T *const qrow = less == Less::row ? draft + A * a.d_pos : nullptr;
+    Weights<T> w = {target + A * a.t_row, less == Less::row ? draft + A * a.d_pos : nullptr,
+                    less == Less::token ? refused : -1};
     const float u = fmaxf(uniforms[a.D * a.u_pos], 0.f);              // NaN: 0
-    const int segs = VERIFY_WARPS * static_cast<int>(size);
-    bool waited = false;
+    const int mine = static_cast<int>(rank) * warps + warp, segs = warps * static_cast<int>(size);
+    const int64_t v0 = min(static_cast<int64_t>(mine) * a.seg, static_cast<int64_t>(a.vocab));
+    const int64_t v1 = min(v0 + a.seg, static_cast<int64_t>(a.vocab));
     for (int attempt = 0; attempt < 2; ++attempt) {
-        const int64_t v0 = static_cast<int64_t>(rank * VERIFY_WARPS + warp) * a.seg;
-        const int32_t v1 = static_cast<int32_t>(min(v0 + a.seg, static_cast<int64_t>(a.vocab)));
-        double sum = 0;
-#pragma unroll 8
-        for (int64_t v = v0 + lane; v < v1; v += 32)
-            sum += weight_at(prow, qrow, less, refused, static_cast<int32_t>(v));
+        double sum = w.q ? lane_sum<true>(w, v0, v1) : lane_sum<false>(w, v0, v1);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             sum += __shfl_xor_sync(~0u, sum, o);
-        if (!waited)
+        if (attempt == 0)
             cluster_wait();                           // every CTA of the cluster has begun
-        waited = true;
         if (lane < static_cast<int>(size))
-            st_peer(peer_addr(&part[attempt][rank * VERIFY_WARPS + warp], lane), sum);
+            st_peer(peer_addr(&part[attempt][mine], lane), sum);
         cluster_arrive();
         cluster_wait();
 
-        // ---- where the running sum passes u W (every warp for itself)
-        double s0 = 2 * lane < segs ? part[attempt][2 * lane] : 0.0;
-        double s1 = 2 * lane + 1 < segs ? part[attempt][2 * lane + 1] : 0.0;
-        double upto = s0 + s1;                        // inclusive over lanes
+        // ---- where the running sum passes u W (every warp for itself): each
+        // lane takes a run of `per` segments
+        const int per = (segs + 31) / 32;
+        double own = 0;
+        for (int k = lane * per; k < min((lane + 1) * per, segs); ++k)
+            own += part[attempt][k];
+        double upto = own;                            // inclusive over lanes
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const double b = __shfl_up_sync(~0u, upto, o);
@@ -168,8 +201,9 @@ __global__ void __launch_bounds__(VERIFY_THREADS) gdn_verify_drafts_kernel(const
         }
         const double total = __shfl_sync(~0u, upto, 31);
         if (!(total > 0.0)) {
-            if (less != Less::none) {                 // p <= q everywhere: draw from p itself
-                less = Less::none;
+            if (w.q || w.out >= 0) {                  // p <= q everywhere: draw from p itself
+                w.q = nullptr;
+                w.out = -1;
                 continue;
             }
             if (rank == 0 && tid == 0) {
@@ -179,25 +213,27 @@ __global__ void __launch_bounds__(VERIFY_THREADS) gdn_verify_drafts_kernel(const
             return;
         }
         const double goal = static_cast<double>(u) * total;
-        double before = __shfl_up_sync(~0u, upto, 1);
-        before = lane ? before : 0.0;
-        // the first segment past the goal, else the last of positive weight
-        const int mine = before + s0 > goal && s0 > 0 ? 2 * lane : (upto > goal && s1 > 0 ? 2 * lane + 1 : segs);
-        const unsigned over = __ballot_sync(~0u, mine < segs);
-        int segment;
-        double base;
-        if (over) {
-            const int l = __ffs(over) - 1;
-            segment = __shfl_sync(~0u, mine, l);
-            base = __shfl_sync(~0u, segment & 1 ? before + s0 : before, l);
-        } else {
-            const unsigned some = __ballot_sync(~0u, s0 > 0 || s1 > 0);
-            const int l = 31 - __clz(some);
-            segment = __shfl_sync(~0u, s1 > 0 ? 2 * lane + 1 : 2 * lane, l);
-            base = 0;
+        const double before = __shfl_up_sync(~0u, upto, 1);
+        // the first segment of positive weight past the goal, else the last of
+        // positive weight
+        int past = segs, last = -1;
+        double base = lane ? before : 0.0;
+        for (int k = lane * per; k < min((lane + 1) * per, segs) && past == segs; ++k) {
+            const double x = part[attempt][k];
+            if (x > 0) {
+                last = k;
+                if (base + x > goal)
+                    past = k;
+                else
+                    base += x;
+            }
         }
+        const unsigned over = __ballot_sync(~0u, past < segs), some = __ballot_sync(~0u, last >= 0);
+        const int from = over ? __ffs(over) - 1 : 31 - __clz(some);
+        const int segment = __shfl_sync(~0u, over ? past : last, from);
+        base = __shfl_sync(~0u, base, from);
         pdl_trigger();
-        if (segment / VERIFY_WARPS != static_cast<int>(rank))
+        if (segment / warps != static_cast<int>(rank))
             return;
 
         // ---- that segment again, a contiguous run of it per thread
@@ -206,14 +242,13 @@ __global__ void __launch_bounds__(VERIFY_THREADS) gdn_verify_drafts_kernel(const
             last_positive = -1;
         }
         const int64_t g0 = static_cast<int64_t>(segment) * a.seg;
-        const int32_t g1 = static_cast<int32_t>(min(g0 + a.seg, static_cast<int64_t>(a.vocab)));
-        const int32_t each = (a.seg + VERIFY_THREADS - 1) / VERIFY_THREADS;
-        const int64_t r0 = g0 + static_cast<int64_t>(tid) * each;
-        const int32_t r1 = static_cast<int32_t>(min(r0 + each, static_cast<int64_t>(g1)));
-        double own = 0;
+        const int64_t g1 = min(g0 + a.seg, static_cast<int64_t>(a.vocab));
+        const int32_t each = (a.seg + threads - 1) / threads;
+        const int64_t r0 = min(g0 + static_cast<int64_t>(tid) * each, g1), r1 = min(r0 + each, g1);
+        double sum1 = 0;
         for (int64_t v = r0; v < r1; ++v)
-            own += weight_at(prow, qrow, less, refused, static_cast<int32_t>(v));
-        double run = own;
+            sum1 += w.q ? w.template at<true>(v) : w.template at<false>(v);
+        double run = sum1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const double b = __shfl_up_sync(~0u, run, o);
@@ -223,24 +258,24 @@ __global__ void __launch_bounds__(VERIFY_THREADS) gdn_verify_drafts_kernel(const
         if (lane == 31)
             scan[warp] = run;
         __syncthreads();
-        double at = over ? base : 0.0;
+        double at = base;
         for (int k = 0; k < warp; ++k)
             at += scan[k];
-        at += run - own;                              // the weight before this thread's run
-        int32_t last = -1;
+        at += run - sum1;                             // the weight before this thread's run
+        int32_t last_here = -1;
         for (int64_t v = r0; v < r1; ++v) {
-            const double w = weight_at(prow, qrow, less, refused, static_cast<int32_t>(v));
-            if (w > 0) {
-                at += w;
-                last = static_cast<int32_t>(v);
+            const double x = w.q ? w.template at<true>(v) : w.template at<false>(v);
+            if (x > 0) {
+                at += x;
+                last_here = static_cast<int32_t>(v);
                 if (over && at > goal) {
-                    atomicMin(&first_over, last);
+                    atomicMin(&first_over, last_here);
                     break;
                 }
             }
         }
-        if (last >= 0)
-            atomicMax(&last_positive, last);
+        if (last_here >= 0)
+            atomicMax(&last_positive, last_here);
         __syncthreads();
         if (tid == 0)
             out[A * a.o_pos] = first_over != INT32_MAX ? first_over : last_positive;
