@@ -307,7 +307,9 @@ GDN_API int gdn_verify_drafts(const gdn_tensor *target_probs, const gdn_tensor *
     const int cluster = verify_cluster(N, vocab, sms);
     const int threads = threads_for(N * cluster, vocab / cluster / 8, sms);
     const int64_t segs = static_cast<int64_t>(cluster) * (threads / 32);
-    p.seg = static_cast<int32_t>(((vocab + segs - 1) / segs + 31) / 32 * 32);
+    const int64_t warp_words = 32 * 16 / elem_size(target_probs->dtype);
+    const int64_t skewed = aligned(target_probs->data, 16) && stride_ok(L.T_tot, L.tok, warp_words / 32) ? 0 : 7;
+    p.seg = static_cast<int32_t>(((vocab + skewed + segs - 1) / segs + warp_words - 1) / warp_words * warp_words);
     const cudaStream_t stream = stream_of(extra);
     const bool pdl = (flags & GDN_LAUNCH_PDL) != 0;
     return status_from(target_probs->dtype == GDN_DTYPE_BF16

@@ -34,7 +34,8 @@ struct Sums {
 };
 __device__ __forceinline__ Sums cta_scan(Sums x, Sums *warp_sums)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = warp_index();
+    __syncwarp();
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long t = __shfl_up_sync(~0u, x.tok, o), b = __shfl_up_sync(~0u, x.blk, o);
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(MAPS_THREADS) gdn_step_maps_kernel(const MapsP
     __shared__ int32_t begin[MAPS_THREADS], fresh_at[MAPS_THREADS];
     __shared__ int32_t warp_max[32];
     __shared__ long long cut_tok, cut_blk;                 // sums before the first request that does not fit
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = warp_index();
     const long long row0 = static_cast<long long>(blockIdx.x) * MAPS_THREADS;
 
     pdl_wait();
@@ -173,6 +174,7 @@ __global__ void __launch_bounds__(MAPS_THREADS) gdn_step_maps_kernel(const MapsP
 
     // ---- each row's request: the last mark at or before it
     int32_t h = mark[tid] >= 0 ? tid : -1;
+    __syncwarp();
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int32_t b = __shfl_up_sync(~0u, h, o);

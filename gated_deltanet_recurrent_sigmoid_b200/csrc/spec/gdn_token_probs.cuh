@@ -58,14 +58,15 @@ struct Sum {
 template <typename Op>
 __device__ __forceinline__ float over_cluster(float x, ProbsShared &sh, int slot, uint32_t rank, uint32_t size)
 {
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int lane = threadIdx.x & 31, warp = warp_index();
+    __syncwarp();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         x = Op::of(x, __shfl_xor_sync(~0u, x, o));
     if (lane == 0)
-        sh.warp[tid >> 5] = x;
+        sh.warp[warp] = x;
     __syncthreads();
-    if (tid < 32) {
+    if (warp == 0) {
         x = lane < static_cast<int>(blockDim.x >> 5) ? sh.warp[lane] : Op::EMPTY;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(PROBS_MAX_THREADS) gdn_token_probs_kernel(cons
     const float t = p.temperature ? p.temperature[ti * p.t_stride] : 1.f;
     const bool bad = !(t >= 0.f) || isinf(t), greedy = t == 0.f;
     // log2(e) / t, at most 1e38 so that 0 * c is 0
-    const float c = greedy || bad ? 0.f : fminf(static_cast<float>(1.4426950408889634 / static_cast<double>(t)), 1e38f);
+    const float c = greedy || bad ? 0.f : fminf(1.44269504f / t, 1e38f);
     if (bad && rank == 0 && tid == 0)
         report(p.status, GDN_DEV_BAD_TEMPERATURE);
     __syncthreads();
