@@ -142,68 +142,103 @@ struct Weights {
     }
 };
 
-// This lane's share of the sum over a segment of the row.  The segment is
-// counted from the 16-byte boundary at or before the row, `skew` elements
-// before it: x0 <= v + skew < x1, x0 a multiple of a warp's 16-byte words, so
-// that all but the row's first and last word are loaded whole.  Where q lies
-// differently in its words both rows are loaded element by element.
+// The whole words among the U at v, v + step, ...: loaded if they lie inside
+// [v0, v1), else zeros, which weigh nothing.
+template <bool ROW, int U, typename T>
+struct Words {
+    static constexpr int E = Elem<T>::PER16;
+    uint4 p[U], q[ROW ? U : 1];
+    __device__ __forceinline__ void load(const Weights<T> &w, int32_t v, int32_t step, int32_t v0, int32_t v1)
+    {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int32_t at = v + k * step;
+            const bool in = at >= v0 && at + E <= v1;
+            p[k] = in ? __ldg(reinterpret_cast<const uint4 *>(w.p + at)) : make_uint4(0, 0, 0, 0);
+            if (ROW)
+                q[k] = in ? __ldg(reinterpret_cast<const uint4 *>(w.q + at)) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    __device__ __forceinline__ void add_to(PairSum (&s)[2], const Weights<T> &w, int32_t v, int k) const
+    {
+        float pf[E], qf[E];
+        unpack16(p[k], pf, static_cast<const T *>(nullptr));
+        if (ROW)
+            unpack16(q[ROW ? k : 0], qf, static_cast<const T *>(nullptr));
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            s[j & 1].template weight<ROW>(pf[j], ROW ? qf[j] : 0.f, ROW || v + j != w.out);
+    }
+};
+
+// Whether the rows lie alike in their 16-byte words.
 template <bool ROW, typename T>
-__device__ __forceinline__ PairSum lane_sum(const Weights<T> &w, int32_t x0, int32_t x1, int32_t skew, int32_t vocab)
+__device__ __forceinline__ bool alike(const Weights<T> &w)
 {
-    constexpr int E = Elem<T>::PER16, U = 4;         // elements a word, words in flight a lane
+    return !ROW || ((reinterpret_cast<uintptr_t>(w.p) ^ reinterpret_cast<uintptr_t>(w.q)) & 15u) == 0;
+}
+
+// A segment of the row, [v0, v1): v0 is the row's begin or the begin of a
+// 16-byte word, v1 the row's end or the end of a word.  The words that the row
+// shares with its neighbours are added element by element.
+// This lane's share of the sum: every 32nd word, or element where the rows lie
+// differently.
+template <bool ROW, typename T>
+__device__ __forceinline__ PairSum lane_sum(const Weights<T> &w, int32_t v0, int32_t v1, int32_t skew)
+{
+    constexpr int E = Elem<T>::PER16, U = ROW ? 4 : 8;   // elements a word, words in flight a lane
     const int lane = threadIdx.x & 31;
     PairSum s[2];
-    if (ROW && ((reinterpret_cast<uintptr_t>(w.p) ^ reinterpret_cast<uintptr_t>(w.q)) & 15u) != 0) {
-        const int32_t v1 = min(x1 - skew, vocab);
+    if (!alike<ROW>(w)) {
 #pragma unroll 8
-        for (int32_t v = max(x0 - skew, 0) + lane; v < v1; v += 32)
+        for (int32_t v = v0 + lane; v < v1; v += 32)
             w.template add_to<ROW>(s[0], v);
         return s[0];
     }
-    for (int32_t x = x0 + lane * E; x < x1; x += 32 * E * U) {
-        uint4 p[U], q[U];
+    const int32_t lead = (E - (v0 + skew) % E) % E, first = v0 + lead;   // elements before the first whole word
+    for (int32_t v = first; v < v1; v += 32 * E * U) {
+        Words<ROW, U, T> x;
+        x.load(w, v + lane * E, 32 * E, v0, v1);
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int32_t v = x - skew + 32 * E * k;
-            const bool whole = x + 32 * E * k < x1 && v >= 0 && v + E <= vocab;
-            p[k] = whole ? __ldg(reinterpret_cast<const uint4 *>(w.p + v)) : make_uint4(0, 0, 0, 0);
-            if (ROW)
-                q[k] = whole ? __ldg(reinterpret_cast<const uint4 *>(w.q + v)) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            float pf[E], qf[E];
-            unpack16(p[k], pf, static_cast<const T *>(nullptr));
-            if (ROW)
-                unpack16(q[k], qf, static_cast<const T *>(nullptr));
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-                s[j & 1].template weight<ROW>(pf[j], ROW ? qf[j] : 0.f, ROW || x - skew + 32 * E * k + j != w.out);
-        }
+        for (int k = 0; k < U; ++k)
+            if (v + 32 * E * k < v1)
+                x.add_to(s, w, v + lane * E + 32 * E * k, k);
     }
-    // the row's first and last word, where they are not whole: with the lane
-    // that they would have gone to
-    const int32_t first = skew ? E - skew : 0;       // elements before the first whole word
-    const int32_t last = max((vocab + skew) / E * E - skew, first);   // the first behind the last whole one
-    if (x0 == 0 && lane == 0)
-        for (int32_t v = 0; v < min(first, vocab); ++v)
-            w.template add_to<ROW>(s[0], v);
-    if (last < vocab && x0 <= last + skew && last + skew < x1 && lane == (last + skew) / E % 32)
-        for (int32_t v = last; v < vocab; ++v)
-            w.template add_to<ROW>(s[0], v);
+    const int32_t last = v1 - (v1 + skew) % E;           // the first element behind the last whole word
+    if (lane < lead && v0 + lane < v1)
+        w.template add_to<ROW>(s[0], v0 + lane);
+    if (last >= first && last + lane < v1)
+        w.template add_to<ROW>(s[0], last + lane);
     s[0].add(s[1]);
     return s[0];
 }
 
-// The sum over v0 <= v < v1 by one thread.
+// The sum over [v0, v1) by one thread, in the row's words as above.
 template <bool ROW, typename T>
-__device__ __forceinline__ PairSum run_sum(const Weights<T> &w, int64_t v0, int64_t v1)
+__device__ __forceinline__ PairSum run_sum(const Weights<T> &w, int32_t v0, int32_t v1, int32_t skew)
 {
-    PairSum s;
-#pragma unroll 8
-    for (int64_t v = v0; v < v1; ++v)
-        w.template add_to<ROW>(s, v);
-    return s;
+    constexpr int E = Elem<T>::PER16, U = 4;
+    PairSum s[2];
+    int32_t v = v0;
+    if (alike<ROW>(w)) {
+        const int32_t lead = min((E - (v0 + skew) % E) % E, max(v1 - v0, 0));
+        for (int32_t j = 0; j < lead; ++j)
+            w.template add_to<ROW>(s[0], v0 + j);
+        for (v += lead; v + E <= v1; v += E * U) {
+            Words<ROW, U, T> x;
+            x.load(w, v, E, v0, v1);
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (v + E * k + E <= v1)
+                    x.add_to(s, w, v + E * k, k);
+        }
+        v = max(v1 - (v1 + skew) % E, v0 + lead);
+    }
+#pragma unroll 4
+    for (; v < v1; ++v)
+        w.template add_to<ROW>(s[0], v);
+    s[0].add(s[1]);
+    return s[0];
 }
 
 template <typename T>
@@ -294,10 +329,14 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS) gdn_verify_drafts_kernel(c
                     less == Less::token ? refused : -1};
     const int mine = static_cast<int>(rank) * warps + warp, segs = warps * static_cast<int>(size);
     const int32_t skew = static_cast<int32_t>((reinterpret_cast<uintptr_t>(w.p) & 15u) / sizeof(T));
-    const int32_t x1 = static_cast<int32_t>(min((static_cast<int64_t>(mine) + 1) * a.seg, static_cast<int64_t>(a.vocab) + skew));
-    const int32_t x0 = static_cast<int32_t>(min(static_cast<int64_t>(mine) * a.seg, static_cast<int64_t>(x1)));
+    // segments are counted from the 16-byte boundary at or before the row
+    auto begin_of = [&](int segment) {
+        return static_cast<int32_t>(min(max(static_cast<int64_t>(segment) * a.seg - skew, static_cast<int64_t>(0)),
+                                        static_cast<int64_t>(a.vocab)));
+    };
+    const int32_t v0 = begin_of(mine), v1 = begin_of(mine + 1);
     for (int attempt = 0; attempt < 2; ++attempt) {
-        PairSum sum = w.q ? lane_sum<true>(w, x0, x1, skew, a.vocab) : lane_sum<false>(w, x0, x1, skew, a.vocab);
+        PairSum sum = w.q ? lane_sum<true>(w, v0, v1, skew) : lane_sum<false>(w, v0, v1, skew);
         __syncwarp();
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -364,14 +403,14 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS) gdn_verify_drafts_kernel(c
         if (segment / warps != static_cast<int>(rank))
             return;
 
-        // ---- that segment again: each thread sums a contiguous run, and the
-        // one whose run holds the token goes through it element by element
+        // ---- that segment again: each thread sums a contiguous run of it
         const PairSum goal = goal_at[0];
-        const int64_t g0 = max(static_cast<int64_t>(segment) * a.seg - skew, static_cast<int64_t>(0));
-        const int64_t g1 = min(static_cast<int64_t>(segment + 1) * a.seg - skew, static_cast<int64_t>(a.vocab));
-        const int32_t each = (a.seg + threads - 1) / threads;
-        const int64_t r0 = min(g0 + static_cast<int64_t>(tid) * each, g1), r1 = min(r0 + each, g1);
-        const PairSum own = w.q ? run_sum<true>(w, r0, r1) : run_sum<false>(w, r0, r1);
+        const int32_t g0 = begin_of(segment), g1 = begin_of(segment + 1);
+        const int32_t each = ((a.seg + threads - 1) / threads + 7) / 8 * 8;      // whole words
+        const int64_t run0 = static_cast<int64_t>(segment) * a.seg + static_cast<int64_t>(tid) * each - skew;
+        const int32_t r0 = static_cast<int32_t>(min(max(run0, static_cast<int64_t>(g0)), static_cast<int64_t>(g1)));
+        const int32_t r1 = static_cast<int32_t>(min(max(run0 + each, static_cast<int64_t>(g0)), static_cast<int64_t>(g1)));
+        const PairSum own = w.q ? run_sum<true>(w, r0, r1, skew) : run_sum<false>(w, r0, r1, skew);
         const PairSum run = warp_upto(own);
         if (lane == 31)
             scan[warp] = run;
@@ -388,19 +427,31 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS) gdn_verify_drafts_kernel(c
             atomicMax(&last_positive, tid);
         }
         __syncthreads();
-        if (tid == (first_over != INT32_MAX ? first_over : last_positive)) {
-            int32_t token = -1;
-            for (int64_t v = r0; v < r1; ++v) {
-                const PairSum x = w.at(v);
-                if (x.positive()) {
-                    token = static_cast<int32_t>(v);
-                    if (at.passes(x, goal))
-                        break;
-                    at.add(x);
-                }
+        // its warp goes through that thread's run, 32 elements at a time
+        const int holder = first_over != INT32_MAX ? first_over : last_positive;
+        if (holder / 32 != warp)
+            return;
+        const int32_t h0 = __shfl_sync(~0u, r0, holder & 31), h1 = __shfl_sync(~0u, r1, holder & 31);
+        PairSum upto = shfl(at, holder & 31);
+        int32_t token = -1;
+        for (int32_t v = h0; v < h1; v += 32) {
+            const PairSum x = v + lane < h1 ? w.at(v + lane) : PairSum{};
+            const PairSum sums = warp_upto(x);
+            PairSum before = shfl_up(sums, 1);
+            PairSum from = upto;
+            from.add(lane ? before : PairSum{});
+            const unsigned some = __ballot_sync(~0u, x.positive()),
+                           over = __ballot_sync(~0u, x.positive() && from.passes(x, goal));
+            if (over) {
+                token = v + __ffs(over) - 1;
+                break;
             }
-            out[A * a.o_pos] = token;
+            if (some)
+                token = v + 31 - __clz(some);
+            upto.add(shfl(sums, 31));
         }
+        if (lane == 0)
+            out[A * a.o_pos] = token;
         return;
     }
 }
