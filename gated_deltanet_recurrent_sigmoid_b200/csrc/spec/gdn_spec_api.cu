@@ -134,11 +134,11 @@ int probs_cluster(int64_t rows, int64_t vocab, int sms)
 }
 
 // CTAs per sequence of a verification: as many (up to 8) as stay resident at
-// once, four of 256 threads an SM, while a CTA keeps 1024 elements.
+// once, eight of 128 threads an SM, while a CTA keeps 1024 elements.
 int verify_cluster(int64_t sequences, int64_t vocab, int sms)
 {
     int c = 1;
-    while (c < 8 && sequences * c * 2 <= 4ll * sms && vocab > c * 1024ll)
+    while (c < 8 && sequences * c * 2 <= 8ll * sms && vocab > c * 1024ll)
         c *= 2;
     return c;
 }
@@ -305,7 +305,8 @@ GDN_API int gdn_verify_drafts(const gdn_tensor *target_probs, const gdn_tensor *
     p.T_tot = static_cast<int32_t>(L.T_tot);
     p.vocab = static_cast<int32_t>(vocab);
     const int cluster = verify_cluster(N, vocab, sms);
-    const int threads = threads_for(N * cluster, vocab / cluster / 8, sms);
+    // 256 threads where the CTAs have an SM each and their lanes a batch of loads
+    const int threads = N * cluster <= sms && vocab > cluster * 8192ll ? 256 : 128;
     const int64_t segs = static_cast<int64_t>(cluster) * (threads / 32);
     const int64_t warp_words = 32 * 16 / elem_size(target_probs->dtype);
     const int64_t skewed = aligned(target_probs->data, 16) && stride_ok(L.T_tot, L.tok, warp_words / 32) ? 0 : 7;

@@ -111,6 +111,23 @@ __device__ __forceinline__ float max16(const uint4 &w, const __nv_bfloat16 *)
     return fmaxf(__low2float(m), __high2float(m));
 }
 
+// The largest of `most` and the word's elements as unsigned bit patterns (both
+// halves of `most` for 16-bit elements), and whether one of them was not a
+// finite number >= 0.
+__device__ __forceinline__ uint32_t most_bits(const uint4 &w, uint32_t most, const float *)
+{
+    return max(max(max(w.x, w.y), max(w.z, w.w)), most);
+}
+__device__ __forceinline__ uint32_t most_bits(const uint4 &w, uint32_t most, const __nv_bfloat16 *)
+{
+    return __vmaxu2(__vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w)), most);
+}
+__device__ __forceinline__ bool beyond_finite(uint32_t most, const float *) { return most >= 0x7f800000u; }
+__device__ __forceinline__ bool beyond_finite(uint32_t most, const __nv_bfloat16 *)
+{
+    return (most & 0xffffu) >= 0x7f80u || most >= 0x7f800000u;
+}
+
 // N consecutive elements of shared memory at an address aligned to
 // min(16, their size) bytes.
 __device__ __forceinline__ void load_group(const float *p, float (&x)[4])

@@ -38,7 +38,7 @@ struct VerifyParams {
     int32_t seg;                     // elements per warp, a multiple of a warp's 16-byte words
 };
 
-constexpr int VERIFY_MAX_THREADS = 1024;
+constexpr int VERIFY_MAX_THREADS = 256;
 constexpr int VERIFY_MAX_WARPS = VERIFY_MAX_THREADS / 32;
 constexpr int VERIFY_MAX_CLUSTER = 8;
 constexpr int VERIFY_MAX_SEGS = VERIFY_MAX_WARPS * VERIFY_MAX_CLUSTER;
@@ -74,6 +74,20 @@ struct PairSum {
             c += in ? e : 0.f;
         } else {
             add(in && counts(p) ? p : 0.f);
+        }
+    }
+    // The same for p (and q) known to be finite and not negative, q <= infinity:
+    // a q above p counts as p.
+    template <bool ROW>
+    __device__ __forceinline__ void weight_of_valid(float p, float q)
+    {
+        if (ROW) {
+            q = fminf(q, p);
+            const float d = p - q;
+            add(d);
+            c += (p - d) - q;
+        } else {
+            add(p);
         }
     }
     __device__ __forceinline__ bool positive() const { return s + c > 0.f; }
@@ -159,6 +173,22 @@ struct Words {
                 q[k] = in ? __ldg(reinterpret_cast<const uint4 *>(w.q + at)) : make_uint4(0, 0, 0, 0);
         }
     }
+    // Word k added without a look at its values; the largest bit patterns say
+    // afterwards whether they were finite and not negative.
+    __device__ __forceinline__ void add_valid(PairSum (&s)[2], uint32_t &most, int k) const
+    {
+        float pf[E], qf[E];
+        unpack16(p[k], pf, static_cast<const T *>(nullptr));
+        most = most_bits(p[k], most, static_cast<const T *>(nullptr));
+        if (ROW) {
+            unpack16(q[ROW ? k : 0], qf, static_cast<const T *>(nullptr));
+            most = most_bits(q[ROW ? k : 0], most, static_cast<const T *>(nullptr));
+        }
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            s[j & 1].template weight_of_valid<ROW>(pf[j], ROW ? qf[j] : 0.f);
+    }
+    // Word k, whose first element is v.
     __device__ __forceinline__ void add_to(PairSum (&s)[2], const Weights<T> &w, int32_t v, int k) const
     {
         float pf[E], qf[E];
@@ -178,39 +208,43 @@ __device__ __forceinline__ bool alike(const Weights<T> &w)
     return !ROW || ((reinterpret_cast<uintptr_t>(w.p) ^ reinterpret_cast<uintptr_t>(w.q)) & 15u) == 0;
 }
 
-// A segment of the row, [v0, v1): v0 is the row's begin or the begin of a
-// 16-byte word, v1 the row's end or the end of a word.  The words that the row
-// shares with its neighbours are added element by element.
-// This lane's share of the sum: every 32nd word, or element where the rows lie
-// differently.
+// This lane's share of the sum over [v0, v1): every 32nd of the words that lie
+// inside whole, the elements around them one by one.  (The row begins `skew`
+// elements behind a 16-byte boundary.)  Where the rows lie differently in
+// their words, or hold values that weigh nothing whatever the other row says
+// (NaN, infinities, negative ones), every 32nd element with a look at each.
 template <bool ROW, typename T>
 __device__ __forceinline__ PairSum lane_sum(const Weights<T> &w, int32_t v0, int32_t v1, int32_t skew)
 {
-    constexpr int E = Elem<T>::PER16, U = ROW ? 4 : 8;   // elements a word, words in flight a lane
+    constexpr int E = Elem<T>::PER16, U = 4;             // elements a word, words in flight a lane
     const int lane = threadIdx.x & 31;
-    PairSum s[2];
-    if (!alike<ROW>(w)) {
-#pragma unroll 8
-        for (int32_t v = v0 + lane; v < v1; v += 32)
-            w.template add_to<ROW>(s[0], v);
-        return s[0];
-    }
-    const int32_t lead = (E - (v0 + skew) % E) % E, first = v0 + lead;   // elements before the first whole word
-    for (int32_t v = first; v < v1; v += 32 * E * U) {
-        Words<ROW, U, T> x;
-        x.load(w, v + lane * E, 32 * E, v0, v1);
+    if (alike<ROW>(w)) {
+        PairSum s[2];
+        uint32_t most = 0;
+        const int32_t lead = (E - (v0 + skew) % E) % E, first = v0 + lead;   // elements before the first whole word
+        for (int32_t v = first; v < v1; v += 32 * E * U) {
+            Words<ROW, U, T> x;
+            x.load(w, v + lane * E, 32 * E, v0, v1);
 #pragma unroll
-        for (int k = 0; k < U; ++k)
-            if (v + 32 * E * k < v1)
-                x.add_to(s, w, v + lane * E + 32 * E * k, k);
+            for (int k = 0; k < U; ++k)
+                if (v + 32 * E * k < v1)
+                    x.add_valid(s, most, k);
+        }
+        const int32_t last = v1 - (v1 + skew) % E;       // the first element behind the last whole word
+        if (lane < lead && v0 + lane < v1)
+            w.template add_to<ROW>(s[0], v0 + lane);
+        if (last >= first && last + lane < v1)
+            w.template add_to<ROW>(s[0], last + lane);
+        s[0].add(s[1]);
+        __syncwarp();
+        if (!__any_sync(~0u, beyond_finite(most, static_cast<const T *>(nullptr))))
+            return s[0];
     }
-    const int32_t last = v1 - (v1 + skew) % E;           // the first element behind the last whole word
-    if (lane < lead && v0 + lane < v1)
-        w.template add_to<ROW>(s[0], v0 + lane);
-    if (last >= first && last + lane < v1)
-        w.template add_to<ROW>(s[0], last + lane);
-    s[0].add(s[1]);
-    return s[0];
+    PairSum s;
+#pragma unroll 8
+    for (int32_t v = v0 + lane; v < v1; v += 32)
+        w.template add_to<ROW>(s, v);
+    return s;
 }
 
 // The sum over [v0, v1) by one thread, in the row's words as above.
@@ -242,7 +276,7 @@ __device__ __forceinline__ PairSum run_sum(const Weights<T> &w, int32_t v0, int3
 }
 
 template <typename T>
-__global__ void __launch_bounds__(VERIFY_MAX_THREADS) gdn_verify_drafts_kernel(const VerifyParams a)
+__global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kernel(const VerifyParams a)
 {
     __shared__ PairSum part[2][VERIFY_MAX_SEGS];      // segment sums of the cluster, for either attempt
     __shared__ PairSum scan[VERIFY_MAX_WARPS];
@@ -336,7 +370,17 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS) gdn_verify_drafts_kernel(c
     };
     const int32_t v0 = begin_of(mine), v1 = begin_of(mine + 1);
     for (int attempt = 0; attempt < 2; ++attempt) {
-        PairSum sum = w.q ? lane_sum<true>(w, v0, v1, skew) : lane_sum<false>(w, v0, v1, skew);
+        PairSum sum;
+        if (w.q) {
+            sum = lane_sum<true>(w, v0, v1, skew);
+        } else {                                      // around the token that weighs nothing
+            const bool cut = w.out >= v0 && w.out < v1;
+            for (int32_t from = v0, to = cut ? w.out : v1;; from = to + 1, to = v1) {
+                sum.add(lane_sum<false>(w, from, to, skew));
+                if (to == v1)
+                    break;
+            }
+        }
         __syncwarp();
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -386,7 +430,7 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS) gdn_verify_drafts_kernel(c
             }
         }
         __syncthreads();
-        const int segment = chosen;
+        const int segment = __shfl_sync(~0u, chosen, 0);
         if (segment < 0) {
             if (w.q || w.out >= 0) {                  // p <= q everywhere: draw from p itself
                 w.q = nullptr;
@@ -428,7 +472,7 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS) gdn_verify_drafts_kernel(c
         }
         __syncthreads();
         // its warp goes through that thread's run, 32 elements at a time
-        const int holder = first_over != INT32_MAX ? first_over : last_positive;
+        const int holder = __shfl_sync(~0u, first_over != INT32_MAX ? first_over : last_positive, 0);
         if (holder / 32 != warp)
             return;
         const int32_t h0 = __shfl_sync(~0u, r0, holder & 31), h1 = __shfl_sync(~0u, r1, holder & 31);
