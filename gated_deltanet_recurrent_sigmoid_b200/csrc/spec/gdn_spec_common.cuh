@@ -26,9 +26,11 @@ __device__ __forceinline__ void report(uint32_t *status, uint32_t bits)
 // (measured), which __syncwarp() behind a loop avoids as well.
 __device__ __forceinline__ int warp_index() { return __shfl_sync(~0u, static_cast<int>(threadIdx.x >> 5), 0); }
 
-// ---- clusters.  Every thread of every CTA takes part in each barrier, its
-// warp as one (__syncwarp() behind code that lanes may have left at different
-// times).
+// ---- clusters.  A CTA learns of its peers' values by mbarriers in its own
+// shared memory, which the peers' stores complete (st_peer): a cluster-wide
+// barrier per exchange was measured to cost more than the stores, most of it
+// in the fence of its release.  The barrier below runs once, behind the
+// initialisation of those mbarriers.
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -41,15 +43,54 @@ __device__ __forceinline__ uint32_t cluster_size()
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_arrive()
+// Every thread of every CTA arrives and waits, its warp as one.  Warps that
+// have nothing to publish arrive relaxed.
+__device__ __forceinline__ void cluster_arrive(bool publishes)
 {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (publishes)
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    else
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait()
 {
     __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A CTA that has given up a wait ends here: its peers may still store into its
+// shared memory, so it stays until each of them has exited or is here too.
+__device__ __forceinline__ void cluster_leave()
+{
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+
+// Bounded wait for phase 0, as sync::mbar_wait, that makes the peers' stores
+// visible.
+__device__ __forceinline__ bool mbar_try_peers(unsigned long long *bar)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(sync::smem_addr(bar))
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_peers(unsigned long long *bar)
+{
+    if (mbar_try_peers(bar))
+        return true;
+    const uint64_t t0 = sync::global_ns();
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_peers(bar))
+            return true;
+        if ((n & 63u) == 0u && sync::global_ns() - t0 > sync::WAIT_LIMIT_NS)
+            return false;
+    }
 }
 
 // Address of this CTA's shared variable `p` in CTA `rank` of the cluster.
@@ -59,13 +100,18 @@ __device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(sync::smem_addr(p)), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void st_peer(uint32_t addr, float x)
+// Store to a peer's shared memory; completes 4 or 8 bytes on its mbarrier.
+__device__ __forceinline__ void st_peer(uint32_t addr, float x, uint32_t bar)
 {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+                 "r"(__float_as_uint(x)), "r"(bar)
+                 : "memory");
 }
-__device__ __forceinline__ void st_peer(uint32_t addr, float x, float y)
+__device__ __forceinline__ void st_peer(uint32_t addr, float x, float y, uint32_t bar)
 {
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(addr),
+                 "r"(__float_as_uint(x)), "r"(__float_as_uint(y)), "r"(bar)
+                 : "memory");
 }
 
 // ---- elements

@@ -36,7 +36,9 @@ constexpr int PROBS_MAX_CLUSTER = 8;
 struct ProbsShared {
     float cta[3][PROBS_MAX_CLUSTER];                       // one value of each CTA of the cluster, per reduction
     float warp[PROBS_MAX_THREADS / 32];
-    unsigned long long full[PROBS_MAX_PIECES];
+    float result;
+    unsigned long long full[PROBS_MAX_PIECES];             // the slice's pieces
+    unsigned long long got[3];                             // the peers' values, per reduction
     int failed;
     alignas(16) unsigned char raw[1];                      // the slice, at its global address modulo 16
 };
@@ -54,7 +56,8 @@ struct Sum {
 };
 
 // Over all threads of the cluster, the same bits in each of them (the order is
-// fixed).  `slot`: which of sh.cta, not used again in the kernel.
+// fixed).  `slot`: which of sh.cta, not used again in the kernel.  A wait that
+// gives up leaves sh.failed set, and a value that is the same in the CTA.
 template <typename Op>
 __device__ __forceinline__ float over_cluster(float x, ProbsShared &sh, int slot, uint32_t rank, uint32_t size)
 {
@@ -72,14 +75,21 @@ __device__ __forceinline__ float over_cluster(float x, ProbsShared &sh, int slot
         for (int o = 16; o > 0; o >>= 1)
             x = Op::of(x, __shfl_xor_sync(~0u, x, o));
         if (lane < static_cast<int>(size))
-            st_peer(peer_addr(&sh.cta[slot][rank], lane), x);
+            st_peer(peer_addr(&sh.cta[slot][rank], lane), x, peer_addr(&sh.got[slot], lane));
+        const bool in = mbar_wait_peers(&sh.got[slot]);
+        __syncwarp();
+        x = lane < static_cast<int>(size) ? sh.cta[slot][lane] : Op::EMPTY;
+#pragma unroll
+        for (int o = PROBS_MAX_CLUSTER / 2; o > 0; o >>= 1)
+            x = Op::of(x, __shfl_xor_sync(~0u, x, o));
+        if (lane == 0) {
+            sh.result = x;
+            if (!in)
+                sh.failed = 1;
+        }
     }
-    cluster_arrive();
-    cluster_wait();
-    x = sh.cta[slot][0];
-    for (uint32_t i = 1; i < size; ++i)
-        x = Op::of(x, sh.cta[slot][i]);
-    return x;
+    __syncthreads();
+    return sh.result;
 }
 
 // 2^((x - m) c) up to a factor that is the same for the whole row.  fast:
@@ -97,11 +107,19 @@ __global__ void __launch_bounds__(PROBS_MAX_THREADS) gdn_token_probs_kernel(cons
     extern __shared__ __align__(16) unsigned char smem[];
     ProbsShared &sh = *reinterpret_cast<ProbsShared *>(smem);
     constexpr int PI = Elem<TIn>::PER16, PO = Elem<TOut>::PER16;
-    const int tid = threadIdx.x, threads = blockDim.x;
+    const int tid = threadIdx.x, threads = static_cast<int>(blockDim.x);
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int64_t row = blockIdx.x / size;
 
-    cluster_arrive();                                      // peers' shared memory is up (waited for below)
+    if (tid == 0) {
+        sh.failed = 0;
+        for (int i = 0; i < 3; ++i) {
+            sync::mbar_init(&sh.got[i], 1);
+            sync::mbar_arrive_expect_tx(&sh.got[i], size * sizeof(float));
+        }
+        sync::fence_barrier_init();
+    }
+    cluster_arrive(warp_index() == 0);                     // waited for before the first exchange
     pdl_wait();
 
     // ---- which row, whose temperature.  A row left out is left out by its
@@ -131,7 +149,6 @@ __global__ void __launch_bounds__(PROBS_MAX_THREADS) gdn_token_probs_kernel(cons
     const uint32_t b0 = off ? 16u : 0u, b1 = max(b0, (off + bytes) & ~15u);   // the words, as offsets in raw
     const int pieces = static_cast<int>((b1 - b0 + PROBS_PIECE - 1) / PROBS_PIECE);
     if (tid == 0) {
-        sh.failed = 0;
         for (int i = 0; i < pieces; ++i)
             sync::mbar_init(&sh.full[i], 1);
         sync::fence_barrier_init();
@@ -175,10 +192,8 @@ __global__ void __launch_bounds__(PROBS_MAX_THREADS) gdn_token_probs_kernel(cons
         for (int w = k * (PROBS_PIECE / 16) + tid; w < w1; w += threads)
             top = fmaxf(top, max16(words[w], static_cast<const TIn *>(nullptr)));
     }
-    if (!ok) {
+    if (!ok)
         sh.failed = 1;
-        report(p.status, GDN_DEV_TIMEOUT);
-    }
     cluster_wait();
     top = over_cluster<Max>(top, sh, 0, rank, size);
 
@@ -224,9 +239,11 @@ __global__ void __launch_bounds__(PROBS_MAX_THREADS) gdn_token_probs_kernel(cons
         }
     }
     pdl_trigger();
+    // (a wait may have given up in one thread alone)
+    const bool failed = __syncthreads_or(sh.failed);
 
     // ---- the probabilities, 16 bytes at a time
-    if (!sh.failed) {
+    if (!failed) {
         TOut *const dst = static_cast<TOut *>(p.probs) + row * p.p_row + e0;
         const int32_t skew = static_cast<int32_t>((reinterpret_cast<uintptr_t>(dst) & 15u) / sizeof(TOut));
         const int32_t first = min(n, skew ? PO - skew : 0);          // elements before the first 16-byte group
@@ -271,11 +288,13 @@ __global__ void __launch_bounds__(PROBS_MAX_THREADS) gdn_token_probs_kernel(cons
             write([&](int32_t, float x) { return power.careful(x) * inv; });
     } else {
         // copies still in flight must land before the CTA's memory goes
+        if (tid == 0)
+            report(p.status, GDN_DEV_TIMEOUT);
         for (int i = tid; i < pieces; i += threads) {
             int never = 0;
             sync::mbar_wait(&sh.full[i], 0, &never);
         }
-        __syncthreads();
+        cluster_leave();
     }
 }
 

@@ -281,12 +281,21 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
     __shared__ PairSum part[2][VERIFY_MAX_SEGS];      // segment sums of the cluster, for either attempt
     __shared__ PairSum scan[VERIFY_MAX_WARPS];
     __shared__ PairSum goal_at[2];                   // u W, and the sum before the chosen segment
-    __shared__ int chosen, first_over, last_positive;
+    __shared__ unsigned long long got[2];            // the cluster's segment sums are in
+    __shared__ int chosen, first_over, last_positive, failed;
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_index(), threads = blockDim.x, warps = threads >> 5;
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int32_t i = static_cast<int32_t>(blockIdx.x / size);
 
-    cluster_arrive();
+    if (tid == 0) {
+        failed = 0;
+        for (int k = 0; k < 2; ++k) {
+            sync::mbar_init(&got[k], 1);
+            sync::mbar_arrive_expect_tx(&got[k], static_cast<uint32_t>(warps) * size * sizeof(PairSum));
+        }
+        sync::fence_barrier_init();
+    }
+    cluster_arrive(warp == 0);                        // waited for before the first exchange
     pdl_wait();
 
     // what does not depend on the sequence's rows is loaded beside them
@@ -386,15 +395,15 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
         for (int o = 16; o > 0; o >>= 1)
             sum.add(PairSum{__shfl_xor_sync(~0u, sum.s, o), __shfl_xor_sync(~0u, sum.c, o)});
         if (attempt == 0)
-            cluster_wait();                           // every CTA of the cluster has begun
+            cluster_wait();                           // every CTA's mbarriers are there
         if (lane < static_cast<int>(size))
-            st_peer(peer_addr(&part[attempt][mine], lane), sum.s, sum.c);
-        cluster_arrive();
-        cluster_wait();
+            st_peer(peer_addr(&part[attempt][mine], lane), sum.s, sum.c, peer_addr(&got[attempt], lane));
 
         // ---- where the running sum passes u W: each lane of the first warp
         // takes a run of `per` segments
         if (warp == 0) {
+            const bool in = mbar_wait_peers(&got[attempt]);
+            __syncwarp();
             const int per = (segs + 31) / 32, k0 = lane * per, k1 = min(k0 + per, segs);
             PairSum own;
             for (int k = k0; k < k1; ++k)
@@ -423,13 +432,21 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
             base = shfl(base, from);
             if (lane == 0) {
                 chosen = segment;                     // -1: no weight at all
+                failed = !in;
                 goal_at[0] = over ? goal : PairSum{INFINITY, 0.f};
                 goal_at[1] = base;
                 first_over = INT32_MAX;
                 last_positive = -1;
             }
         }
-        __syncthreads();
+        if (__syncthreads_or(failed)) {
+            if (rank == 0 && tid == 0) {
+                out[A * a.o_pos] = -1;
+                report(a.status, GDN_DEV_TIMEOUT);
+            }
+            cluster_leave();
+            return;
+        }
         const int segment = __shfl_sync(~0u, chosen, 0);
         if (segment < 0) {
             if (w.q || w.out >= 0) {                  // p <= q everywhere: draw from p itself
