@@ -66,27 +66,26 @@ __device__ __forceinline__ void cluster_leave()
     asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
-// Bounded wait for phase 0, as sync::mbar_wait, that makes the peers' stores
-// visible.
-__device__ __forceinline__ bool mbar_try_peers(unsigned long long *bar)
+// Bounded wait, as sync::mbar_wait, that makes the peers' stores visible.
+__device__ __forceinline__ bool mbar_try_peers(unsigned long long *bar, uint32_t parity)
 {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(sync::smem_addr(bar))
+        : "r"(sync::smem_addr(bar)), "r"(parity)
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ bool mbar_wait_peers(unsigned long long *bar)
+__device__ __forceinline__ bool mbar_wait_peers(unsigned long long *bar, uint32_t parity)
 {
-    if (mbar_try_peers(bar))
+    if (mbar_try_peers(bar, parity))
         return true;
     const uint64_t t0 = sync::global_ns();
     for (uint32_t n = 1;; ++n) {
-        if (mbar_try_peers(bar))
+        if (mbar_try_peers(bar, parity))
             return true;
         if ((n & 63u) == 0u && sync::global_ns() - t0 > sync::WAIT_LIMIT_NS)
             return false;

@@ -1,12 +1,13 @@
 // gdn_step_maps.cuh -- a step's index arrays from its requests' lengths
 // (gdn_step_maps in include/gdn_spec.h).
 //
-// Two exclusive sums over the requests (tokens, new blocks) and one row of
-// output per token.  One launch: every CTA sums all N requests for itself (a
-// few KB from L2) instead of waiting for another, marks where the requests
-// that cross its 1024 packed rows begin, and a running maximum over the marks
-// tells each row its request.  Bound by latency, then by the 16 bytes written
-// per row.
+// Two running sums over the requests (tokens, new blocks) and one row of output
+// per token.  One launch: every CTA sums all N requests for itself (a few KB
+// from L2) instead of waiting for another, marks where the requests that cross
+// its 1024 packed rows begin, and a running maximum over the marks tells each
+// row its request.  A thread takes four requests and four rows at a time, so
+// the rows' 16 bytes are written as whole words.  Bound by latency: two global
+// loads one behind the other (the request, its block), then the stores.
 #pragma once
 
 #include "gdn_spec_common.cuh"
@@ -26,146 +27,163 @@ struct MapsParams {
     int32_t N, C, B, F, block_size, blocked;
 };
 
-constexpr int MAPS_THREADS = 1024;         // = packed rows a CTA = requests a scan step
+constexpr int MAPS_THREADS = 256;
+constexpr int MAPS_WARPS = MAPS_THREADS / 32;
 
-// Inclusive sums over the CTA of (tokens, blocks) per thread.
+// Running sums of (tokens, new blocks).
 struct Sums {
     long long tok, blk;
+    __device__ __forceinline__ void add(const Sums &x)
+    {
+        tok += x.tok;
+        blk += x.blk;
+    }
 };
-__device__ __forceinline__ Sums cta_scan(Sums x, Sums *warp_sums)
+
+// The sums over the threads before this one, and over all of them in `all`.
+__device__ __forceinline__ Sums cta_before(const Sums &own, Sums *warp_sums, Sums *all)
 {
     const int lane = threadIdx.x & 31, warp = warp_index();
+    Sums x = own;
     __syncwarp();
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(~0u, x.tok, o), b = __shfl_up_sync(~0u, x.blk, o);
-        if (lane >= o) {
-            x.tok += t;
-            x.blk += b;
-        }
+        const Sums b = {__shfl_up_sync(~0u, x.tok, o), __shfl_up_sync(~0u, x.blk, o)};
+        if (lane >= o)
+            x.add(b);
     }
     if (lane == 31)
         warp_sums[warp] = x;
     __syncthreads();
-    if (warp == 0) {
-        Sums w = warp_sums[lane];
+    Sums before = {x.tok - own.tok, x.blk - own.blk};
+    *all = {0, 0};
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(~0u, w.tok, o), b = __shfl_up_sync(~0u, w.blk, o);
-            if (lane >= o) {
-                w.tok += t;
-                w.blk += b;
-            }
-        }
-        warp_sums[lane] = w;
+    for (int w = 0; w < MAPS_WARPS; ++w) {
+        if (w < warp)
+            before.add(warp_sums[w]);
+        all->add(warp_sums[w]);
     }
-    __syncthreads();
-    if (warp > 0) {
-        x.tok += warp_sums[warp - 1].tok;
-        x.blk += warp_sums[warp - 1].blk;
-    }
-    return x;
+    return before;
 }
 
+// What the rows of a request need of it.
+struct MapsRequest {
+    int32_t seq, begin, context, held, fresh;      // fresh: where its new blocks begin in free_blocks
+};
+
+// EACH: requests of a scan step, and rows, per thread.
+template <int EACH>
 __global__ void __launch_bounds__(MAPS_THREADS) gdn_step_maps_kernel(const MapsParams a)
 {
-    __shared__ Sums warp_sums[32];
-    __shared__ int32_t mark[MAPS_THREADS];                 // request that begins (or goes on) at this row, or -1
-    __shared__ int32_t begin[MAPS_THREADS], fresh_at[MAPS_THREADS];
-    __shared__ int32_t warp_max[32];
-    __shared__ long long cut_tok, cut_blk;                 // sums before the first request that does not fit
+    constexpr int TILE = MAPS_THREADS * EACH;
+    __shared__ Sums warp_sums[2][MAPS_WARPS];
+    __shared__ MapsRequest mark[TILE];                // request that begins, or goes on, at this row; seq -1: none
+    __shared__ int32_t warp_max[MAPS_WARPS];
+    __shared__ Sums cut;                                   // sums before the first request that does not fit; tok -1: all fit
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_index();
-    const long long row0 = static_cast<long long>(blockIdx.x) * MAPS_THREADS;
+    const long long row0 = static_cast<long long>(blockIdx.x) * TILE;
 
     pdl_wait();
-    mark[tid] = -1;
-    if (tid == 0)
-        cut_tok = -1;
     const bool blocks = a.blocked != 0;
     int32_t head = 0;
     long long room = 0;                                    // free blocks left
     uint32_t bad = 0;
-    if (blocks) {
+    if (blocks)
         head = *a.free_head;
-        if (head < 0 || head > a.F) {
-            bad |= GDN_DEV_BAD_BLOCKS;
-            room = -1;                                     // nothing fits
-        } else {
-            room = a.F - head;
-        }
-    }
-    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < EACH; ++e)
+        mark[e * MAPS_THREADS + tid].seq = -1;
+    if (tid == 0)
+        cut = {-1, 0};
 
     Sums base = {0, 0};
-    const int steps = (a.N + MAPS_THREADS - 1) / MAPS_THREADS;
+    const int steps = (a.N + TILE - 1) / TILE;
     for (int k = 0; k < steps; ++k) {
-        const int32_t i = k * MAPS_THREADS + tid;
-        int32_t slot = -1, len = 0, held = 0;
-        Sums mine = {0, 0};
-        if (i < a.N) {
-            slot = a.slots[i];
-            len = a.lengths[i];
-            const int32_t have = a.context[i];
-            uint32_t wrong = 0;
-            if (slot < -1)
-                wrong |= GDN_DEV_BAD_SLOT;
-            if (len < 0 || have < 0 || static_cast<long long>(len) + have > INT32_MAX)
+        const int32_t i0 = k * TILE + tid * EACH;
+        int32_t slot[EACH], len[EACH], have[EACH], held[EACH];
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            const bool in = i0 + e < a.N;
+            slot[e] = in ? a.slots[i0 + e] : -1;
+            len[e] = in ? a.lengths[i0 + e] : 0;
+            have[e] = in ? a.context[i0 + e] : 0;
+            held[e] = in && blocks ? a.held[i0 + e] : 0;
+        }
+        if (k == 0 && blocks) {
+            const bool usable = head >= 0 && head <= a.F;
+            room = usable ? a.F - head : -1;               // -1: nothing fits
+            bad |= usable ? 0u : GDN_DEV_BAD_BLOCKS;
+        }
+        Sums mine[EACH], own = {0, 0};
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            mine[e] = {0, 0};
+            uint32_t wrong = slot[e] < -1 ? GDN_DEV_BAD_SLOT : 0u;
+            if (len[e] < 0 || have[e] < 0 || static_cast<long long>(len[e]) + have[e] > INT32_MAX)
                 wrong |= GDN_DEV_BAD_LENGTH;
-            if (blocks)
-                held = a.held[i];
-            if (slot != -1 && !wrong && len > 0) {
-                mine.tok = len;
+            if (slot[e] != -1 && !wrong && len[e] > 0) {
+                mine[e].tok = len[e];
                 if (blocks) {
-                    const uint32_t need = (static_cast<uint32_t>(have) + len + a.block_size - 1) / static_cast<uint32_t>(a.block_size);
-                    if (held < 0 || held > a.B || static_cast<long long>(held) * a.block_size < have ||
+                    const uint32_t need = (static_cast<uint32_t>(have[e]) + len[e] + a.block_size - 1) /
+                                          static_cast<uint32_t>(a.block_size);
+                    if (held[e] < 0 || held[e] > a.B || static_cast<long long>(held[e]) * a.block_size < have[e] ||
                         need > static_cast<uint32_t>(a.B)) {
                         wrong |= GDN_DEV_BAD_BLOCKS;
-                        mine.tok = 0;
-                    } else if (need > static_cast<uint32_t>(held)) {
-                        mine.blk = need - held;
+                        mine[e].tok = 0;
+                    } else if (need > static_cast<uint32_t>(held[e])) {
+                        mine[e].blk = need - held[e];
                     }
                 }
             }
-            if (slot != -1)
+            if (slot[e] != -1)
                 bad |= wrong;
+            own.add(mine[e]);
         }
-        const Sums own = mine;
-        Sums to = cta_scan(mine, warp_sums);
-        to.tok += base.tok;
-        to.blk += base.blk;
-        const Sums from = {to.tok - own.tok, to.blk - own.blk};
+        Sums all, from = cta_before(own, warp_sums[k & 1], &all);
+        from.add(base);
         // both sums only grow, so what fits is a run of requests from the first
-        const bool fits = to.tok <= a.C && (!blocks || to.blk <= room);
-        const bool fitted = from.tok <= a.C && (!blocks || from.blk <= room);
-        if (i < a.N && !fits && (fitted || (i == 0))) {
-            cut_tok = from.tok;
-            cut_blk = from.blk;
+        auto fits = [&](const Sums &s) { return s.tok <= a.C && (!blocks || s.blk <= room); };
+        Sums to[EACH];
+        Sums at = from;
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            const Sums prior = at;
+            at.add(mine[e]);
+            to[e] = at;
+            if (i0 + e < a.N && !fits(at) && (i0 + e == 0 || fits(prior)))
+                cut = prior;
         }
-        __syncthreads();
-        const bool runs = own.tok > 0 && fits;
-        if (own.tok > 0 && !fits)
-            bad |= GDN_DEV_NO_ROOM;
-        if (i < a.N && k % gridDim.x == blockIdx.x) {
-            a.cu_seqlens[i + 1] = static_cast<int32_t>(fits ? to.tok : cut_tok);
-            a.state_indices[i] = runs ? slot : -1;
-            if (blocks)
-                a.held_out[i] = runs ? held + static_cast<int32_t>(own.blk) : held;
+        base.add(all);
+        const bool whole = fits(base);                     // then no request up to here was cut
+        if (!whole)
+            __syncthreads();
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            const int32_t i = i0 + e;
+            const bool in = whole || fits(to[e]), runs = mine[e].tok > 0 && in;
+            const Sums prior = {to[e].tok - mine[e].tok, to[e].blk - mine[e].blk};
+            if (mine[e].tok > 0 && !in)
+                bad |= GDN_DEV_NO_ROOM;
+            if (i < a.N && k % gridDim.x == blockIdx.x) {
+                a.cu_seqlens[i + 1] = static_cast<int32_t>(in ? to[e].tok : cut.tok);
+                a.state_indices[i] = runs ? slot[e] : -1;
+                if (blocks)
+                    a.held_out[i] = runs ? held[e] + static_cast<int32_t>(mine[e].blk) : held[e];
+            }
+            if (runs && to[e].tok > row0 && prior.tok < row0 + TILE)
+                mark[prior.tok > row0 ? prior.tok - row0 : 0] = {i, static_cast<int32_t>(prior.tok), have[e], held[e],
+                                                                 head + static_cast<int32_t>(prior.blk)};
         }
-        if (runs && to.tok > row0 && from.tok < row0 + MAPS_THREADS) {
-            const int at = from.tok > row0 ? static_cast<int>(from.tok - row0) : 0;
-            mark[at] = i;
-            begin[at] = static_cast<int32_t>(from.tok);
-            fresh_at[at] = head + static_cast<int32_t>(from.blk);
-        }
-        base.tok += warp_sums[31].tok;
-        base.blk += warp_sums[31].blk;
-        __syncthreads();
     }
+    if (steps == 0 && blocks && (head < 0 || head > a.F))
+        bad |= GDN_DEV_BAD_BLOCKS;
+    __syncthreads();                                       // marks and the cut
+    const Sums end = cut.tok >= 0 ? cut : base;
     if (blockIdx.x == 0) {
         if (tid == 0) {
             a.cu_seqlens[0] = 0;
             if (blocks)
-                *a.free_head_out = head + static_cast<int32_t>(cut_tok >= 0 ? cut_blk : base.blk);
+                *a.free_head_out = head + static_cast<int32_t>(end.blk);
         }
         if (bad)
             report(a.status, bad);
@@ -173,7 +191,12 @@ __global__ void __launch_bounds__(MAPS_THREADS) gdn_step_maps_kernel(const MapsP
     pdl_trigger();
 
     // ---- each row's request: the last mark at or before it
-    int32_t h = mark[tid] >= 0 ? tid : -1;
+    const int r0 = tid * EACH;
+    int32_t h = -1;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e)
+        if (mark[r0 + e].seq >= 0)
+            h = r0 + e;
     __syncwarp();
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -183,35 +206,59 @@ __global__ void __launch_bounds__(MAPS_THREADS) gdn_step_maps_kernel(const MapsP
     }
     if (lane == 31)
         warp_max[warp] = h;
+    h = __shfl_up_sync(~0u, h, 1);
+    h = lane ? h : -1;                                     // before this thread's rows, in its warp
     __syncthreads();
-    for (int w = 0; w < warp; ++w)
-        h = max(h, warp_max[w]);
-    const long long total = cut_tok >= 0 ? cut_tok : base.tok;
-    const long long t = row0 + tid;
-    if (t >= a.C)
+#pragma unroll
+    for (int w = 0; w < MAPS_WARPS; ++w)
+        if (w < warp)
+            h = max(h, warp_max[w]);
+    const long long t0 = row0 + r0;
+    if (t0 >= a.C)
         return;
-    int32_t seq = -1, pos = -1;
-    long long place = -1;
-    if (t < total && h >= 0) {
-        seq = mark[h];
-        pos = a.context[seq] + static_cast<int32_t>(t - begin[h]);
-        if (blocks) {
-            const int32_t held = a.held[seq], lb = pos / a.block_size, in = pos - lb * a.block_size;
-            int32_t block;
-            if (lb < held) {
-                block = a.tables[seq * a.b_row + lb];
-            } else {
-                block = a.free_blocks[fresh_at[h] + lb - held];
-                if (in == 0)                               // a new block's first token
-                    a.tables[seq * a.b_row + lb] = block;
+    int32_t seq[EACH], pos[EACH], block[EACH], in[EACH];
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+        if (mark[r0 + e].seq >= 0)
+            h = r0 + e;
+        seq[e] = pos[e] = block[e] = -1;
+        in[e] = 0;
+        if (t0 + e < end.tok && h >= 0) {
+            const MapsRequest q = mark[h];
+            seq[e] = q.seq;
+            pos[e] = q.context + static_cast<int32_t>(t0 + e - q.begin);
+            if (blocks) {
+                const int32_t lb = pos[e] / a.block_size;
+                in[e] = pos[e] - lb * a.block_size;
+                block[e] = lb < q.held ? a.tables[q.seq * a.b_row + lb] : a.free_blocks[q.fresh + lb - q.held];
+                if (lb >= q.held && in[e] == 0)            // a new block's first token
+                    a.tables[q.seq * a.b_row + lb] = block[e];
             }
-            place = static_cast<long long>(block) * a.block_size + in;
         }
     }
-    a.row_seq[t] = seq;
-    a.positions[t] = pos;
-    if (blocks)
-        a.slot_map[t] = place;
+    long long place[EACH];
+#pragma unroll
+    for (int e = 0; e < EACH; ++e)
+        place[e] = seq[e] >= 0 ? static_cast<long long>(block[e]) * a.block_size + in[e] : -1;
+    const uintptr_t lie = reinterpret_cast<uintptr_t>(a.row_seq) | reinterpret_cast<uintptr_t>(a.positions) |
+                          reinterpret_cast<uintptr_t>(a.slot_map);
+    if (EACH == 4 && t0 + EACH <= a.C && (lie & 15u) == 0) {
+        *reinterpret_cast<int4 *>(a.row_seq + t0) = make_int4(seq[0], seq[1 % EACH], seq[2 % EACH], seq[3 % EACH]);
+        *reinterpret_cast<int4 *>(a.positions + t0) = make_int4(pos[0], pos[1 % EACH], pos[2 % EACH], pos[3 % EACH]);
+        if (blocks) {
+            *reinterpret_cast<longlong2 *>(a.slot_map + t0) = make_longlong2(place[0], place[1 % EACH]);
+            *reinterpret_cast<longlong2 *>(a.slot_map + t0 + 2) = make_longlong2(place[2 % EACH], place[3 % EACH]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < EACH; ++e)
+            if (t0 + e < a.C) {
+                a.row_seq[t0 + e] = seq[e];
+                a.positions[t0 + e] = pos[e];
+                if (blocks)
+                    a.slot_map[t0 + e] = place[e];
+            }
+    }
 }
 
 }  // namespace spec

@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
         // ---- where the running sum passes u W: each lane of the first warp
         // takes a run of `per` segments
         if (warp == 0) {
-            const bool in = mbar_wait_peers(&got[attempt]);
+            const bool in = mbar_wait_peers(&got[attempt], 0);
             __syncwarp();
             const int per = (segs + 31) / 32, k0 = lane * per, k1 = min(k0 + per, segs);
             PairSum own;

@@ -442,6 +442,7 @@ def test_maps_of_nothing():
     empty = {k: (v[:0] if k in ("lengths", "context", "slots", "tables", "held") else v) for k, v in p.items()}
     check_maps(empty, 1030)
     check_maps({k: empty[k] for k in ("lengths", "context", "slots")}, 3)
+    check_maps({**empty, "head": -1}, 3)
 
 
 @pytest.mark.parametrize("n,longest", [(40, 30), (2100, 5)])
