@@ -83,12 +83,11 @@ bool rows_apart(const gdn_tensor *t) { return t->shape[0] <= 1 || t->stride[0] >
 cudaStream_t stream_of(const gdn_extra *x) { return x ? static_cast<cudaStream_t>(x->stream) : nullptr; }
 uint32_t *status_of(const gdn_extra *x) { return x ? x->device_status : nullptr; }
 
-// A launch of thread-block clusters, with or without the attribute of
-// programmatic dependent launch.
+// A launch of thread-block clusters with programmatic stream serialization.
 struct ClusterLaunch {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    ClusterLaunch(int64_t ctas, int cluster, int threads, size_t smem, cudaStream_t stream, bool pdl)
+    ClusterLaunch(int64_t ctas, int cluster, int threads, size_t smem, cudaStream_t stream)
     {
         cfg.gridDim = dim3(static_cast<unsigned>(ctas));
         cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -101,16 +100,16 @@ struct ClusterLaunch {
         attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = pdl ? 2 : 1;
+        cfg.numAttrs = 2;
     }
     ClusterLaunch(const ClusterLaunch &) = delete;
 };
 
 template <typename Kernel, typename Params>
 cudaError_t launch_cluster(Kernel kernel, int64_t ctas, int cluster, int threads, size_t smem, cudaStream_t stream,
-                           bool pdl, const Params &p)
+                           const Params &p)
 {
-    const ClusterLaunch launch(ctas, cluster, threads, smem, stream, pdl);
+    const ClusterLaunch launch(ctas, cluster, threads, smem, stream);
     return cudaLaunchKernelEx(&launch.cfg, kernel, p);
 }
 
@@ -118,7 +117,7 @@ int status_from(cudaError_t err) { return err == cudaSuccess ? GDN_OK : GDN_ERR_
 
 template <typename TIn, typename TOut>
 cudaError_t launch_probs(const gdn::spec::ProbsParams &p, int64_t rows, int cluster, int threads, size_t smem,
-                         cudaStream_t stream, bool pdl)
+                         cudaStream_t stream)
 {
     static PerDevice once;
     int dev = 0;
@@ -136,7 +135,7 @@ cudaError_t launch_probs(const gdn::spec::ProbsParams &p, int64_t rows, int clus
     uint64_t known = err == cudaSuccess ? resident[dev].load(std::memory_order_relaxed) : 0;
     if (err == cudaSuccess && known >> 32 != shape) {
         int clusters = 0;
-        ClusterLaunch probe(cluster, cluster, threads, smem, nullptr, false);
+        ClusterLaunch probe(cluster, cluster, threads, smem, nullptr);
         err = cudaOccupancyMaxActiveClusters(&clusters, gdn::spec::gdn_token_probs_kernel<TIn, TOut>, &probe.cfg);
         known = shape << 32 | static_cast<uint64_t>(clusters > 0 ? clusters : 1);
         if (err == cudaSuccess)
@@ -148,7 +147,7 @@ cudaError_t launch_probs(const gdn::spec::ProbsParams &p, int64_t rows, int clus
     const int64_t most = static_cast<int64_t>(known & 0xffffffffu), turns = (rows + most - 1) / most;
     const int64_t clusters = (rows + turns - 1) / turns;
     return launch_cluster(gdn::spec::gdn_token_probs_kernel<TIn, TOut>, clusters * cluster, cluster, threads, smem,
-                          stream, pdl, p);
+                          stream, p);
 }
 
 // CTAs per row of token probabilities: slices of at most 16 KB as far as 8 CTAs
@@ -241,13 +240,12 @@ GDN_API int gdn_token_probs(const gdn_tensor *logits, const gdn_tensor *temperat
     const int threads = slice_bytes > 16384 || (R * cluster <= sms && slice_bytes > 4096) ? gdn::spec::PROBS_MAX_THREADS : 128;
     const size_t smem = gdn::spec::probs_smem(slice_bytes);
     const cudaStream_t stream = stream_of(extra);
-    const bool pdl = (flags & GDN_LAUNCH_PDL) != 0;
     const bool in16 = logits->dtype == GDN_DTYPE_BF16, out16 = probs->dtype == GDN_DTYPE_BF16;
     using bf16 = __nv_bfloat16;
-    return status_from(in16 ? (out16 ? launch_probs<bf16, bf16>(p, R, cluster, threads, smem, stream, pdl)
-                                     : launch_probs<bf16, float>(p, R, cluster, threads, smem, stream, pdl))
-                            : (out16 ? launch_probs<float, bf16>(p, R, cluster, threads, smem, stream, pdl)
-                                     : launch_probs<float, float>(p, R, cluster, threads, smem, stream, pdl)));
+    return status_from(in16 ? (out16 ? launch_probs<bf16, bf16>(p, R, cluster, threads, smem, stream)
+                                     : launch_probs<bf16, float>(p, R, cluster, threads, smem, stream))
+                            : (out16 ? launch_probs<float, bf16>(p, R, cluster, threads, smem, stream)
+                                     : launch_probs<float, float>(p, R, cluster, threads, smem, stream)));
 }
 
 GDN_API int gdn_verify_drafts(const gdn_tensor *target_probs, const gdn_tensor *draft_tokens,
@@ -337,12 +335,11 @@ GDN_API int gdn_verify_drafts(const gdn_tensor *target_probs, const gdn_tensor *
     const int64_t skewed = aligned(target_probs->data, 16) && stride_ok(L.T_tot, L.tok, warp_words / 32) ? 0 : 7;
     p.seg = static_cast<int32_t>(((vocab + skewed + segs - 1) / segs + warp_words - 1) / warp_words * warp_words);
     const cudaStream_t stream = stream_of(extra);
-    const bool pdl = (flags & GDN_LAUNCH_PDL) != 0;
     return status_from(target_probs->dtype == GDN_DTYPE_BF16
                            ? launch_cluster(gdn::spec::gdn_verify_drafts_kernel<__nv_bfloat16>, N * cluster, cluster,
-                                            threads, 0, stream, pdl, p)
+                                            threads, 0, stream, p)
                            : launch_cluster(gdn::spec::gdn_verify_drafts_kernel<float>, N * cluster, cluster,
-                                            threads, 0, stream, pdl, p));
+                                            threads, 0, stream, p));
 }
 
 GDN_API int gdn_commit_states(const gdn_tensor *intermediate_states, const gdn_tensor *num_tokens,
@@ -402,7 +399,7 @@ GDN_API int gdn_commit_states(const gdn_tensor *intermediate_states, const gdn_t
     return status_from(launch_ex(gdn::spec::gdn_commit_states_kernel,
                                  dim3(static_cast<unsigned>(N * HV * gdn::spec::COMMIT_PIECES)),
                                  dim3(gdn::spec::COMMIT_THREADS), 0, stream_of(extra),
-                                 (flags & GDN_LAUNCH_PDL) != 0, p));
+                                 true, p));
 }
 
 GDN_API int gdn_step_maps(const gdn_step_maps_call *c)
@@ -480,7 +477,7 @@ GDN_API int gdn_step_maps(const gdn_step_maps_call *c)
     const int64_t tile = gdn::spec::MAPS_THREADS * each, tiles = (C + tile - 1) / tile;
     return status_from(launch_ex(each == 1 ? gdn::spec::gdn_step_maps_kernel<1> : gdn::spec::gdn_step_maps_kernel<4>,
                                  dim3(static_cast<unsigned>(tiles > 0 ? tiles : 1)), dim3(gdn::spec::MAPS_THREADS), 0,
-                                 stream_of(c->extra), (c->flags & GDN_LAUNCH_PDL) != 0, p));
+                                 stream_of(c->extra), true, p));
 }
 
 }  // extern "C"

@@ -11,6 +11,12 @@
 namespace gdn {
 namespace spec {
 
+// Every kernel here is launched with programmatic stream serialization: it may
+// be scheduled while the kernel before it on the stream still runs, and waits
+// (pdl_wait), before it touches global memory, until that one has completed.
+// Late in its own work it lets its successor be scheduled (pdl_trigger).  Back
+// to back this saves 1 to 2.5 us a call (1 x 32768 probabilities 6.1 -> 3.7 us,
+// verification 8.2 -> 5.5; with the trigger at the start 3.7 and 6.0).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -76,6 +76,8 @@ def load() -> ctypes.CDLL:
         lib.gdn_spec_version.argtypes = []
         for name in ("gdn_token_probs", "gdn_verify_drafts", "gdn_commit_states", "gdn_step_maps", "gdn_spec_version"):
             getattr(lib, name).restype = ctypes.c_int
+        # the same functions without argument types: prepared calls pass pointers made once
+        lib.untyped = ctypes.CDLL(path)
         _LIB = lib
     return _LIB
 
@@ -123,15 +125,22 @@ class _Prepared:
             raise GdnError(status, status_string(status))
 
     def _ready(self) -> None:
-        self._fn, self._args = self._bind()
+        fn, args = self._bind()
+        self._bound = args
+        self._fn = getattr(load().untyped, fn.__name__)
+        self._args = tuple(ctypes.c_void_p(ctypes.addressof(a._obj)) if hasattr(a, "_obj") else a for a in args)
+        self._stream = None
 
     def __call__(self) -> None:
+        device = self._device
         if self._follow:
-            self._extra.stream = torch._C._cuda_getCurrentRawStream(self._device)
-        if torch._C._cuda_getDevice() == self._device:
+            stream = torch._C._cuda_getCurrentRawStream(device)
+            if stream != self._stream:
+                self._extra.stream = self._stream = stream
+        if torch._C._cuda_getDevice() == device:
             status = self._fn(*self._args)
         else:
-            with torch.cuda.device(self._device):
+            with torch.cuda.device(device):
                 status = self._fn(*self._args)
         if status != OK:
             raise GdnError(status, status_string(status))

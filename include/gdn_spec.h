@@ -22,7 +22,9 @@
  * nothing, keeps nothing and can be captured in a CUDA graph.  No written
  * tensor may overlap any other tensor of the call (GDN_ERR_ALIAS).  In
  * `extra` only stream and device_status are used; every other field must be 0
- * (GDN_ERR_ARG).  flags: GDN_LAUNCH_PDL, GDN_SPEC_CHECK_ONLY.  The kernels
+ * (GDN_ERR_ARG).  flags: GDN_SPEC_CHECK_ONLY, and GDN_LAUNCH_PDL, which every
+ * call here implies (the kernel may be scheduled while the previous one on the
+ * stream still runs, and waits for it before it touches memory).  The kernels
  * run on the calling thread's current device, which must be the tensors' own.
  *
  * What only the device can see is reported by OR-ing the bits below (and
