@@ -312,7 +312,7 @@ __device__ __forceinline__ PairSum lane_sum(const Weights<T> &w, int32_t v0, int
 template <bool ROW, typename T>
 __device__ __forceinline__ PairSum run_sum(const Weights<T> &w, int32_t v0, int32_t v1, int32_t skew)
 {
-    constexpr int E = Elem<T>::PER16, U = 4;
+    constexpr int E = Elem<T>::PER16, U = ROW ? 4 : 8;
     PairSum s[2];
     int32_t v = v0;
     if (alike<ROW>(w)) {
