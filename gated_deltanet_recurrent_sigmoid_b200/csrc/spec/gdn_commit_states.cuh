@@ -20,7 +20,7 @@ struct CommitParams {
 };
 
 constexpr int COMMIT_THREADS = 256;
-constexpr int COMMIT_VECS = 4;                                     // 16-byte words a thread
+constexpr int COMMIT_VECS = 2;                                     // 16-byte words a thread
 constexpr int COMMIT_PIECES = 128 * 128 / 4 / (COMMIT_THREADS * COMMIT_VECS);
 
 __global__ void __launch_bounds__(COMMIT_THREADS) gdn_commit_states_kernel(const CommitParams a)

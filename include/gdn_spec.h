@@ -105,8 +105,8 @@ GDN_API int gdn_token_probs(const gdn_tensor *logits, const gdn_tensor *temperat
  *                                            (q = 1 at x_j, 0 elsewhere)
  *   uniforms       fp32       [N, D + 1]     any strides; values in [0, 1)
  *   cu_seqlens     int32      [N + 1] or NULL  contiguous; T_i <= D + 1
- *   state_indices  int32      [N] or NULL    contiguous; -1 marks a padded
- *                                            sequence
+ *   state_indices  int32      [N] or NULL    contiguous; a negative one marks a
+ *                                            padded sequence
  *   out_tokens     int32      [N, D + 1]     the accepted drafts, the drawn
  *                                            token, then -1
  *   num_tokens     int32      [N]            A + 1
@@ -115,7 +115,7 @@ GDN_API int gdn_token_probs(const gdn_tensor *logits, const gdn_tensor *temperat
  * its whole row of out_tokens.  draft_tokens[i, j] = -1 ends a sequence's
  * drafts early: the token is drawn from p_j itself; so does any other token
  * outside the vocabulary, with GDN_DEV_BAD_TOKEN.  Comparisons are exact, sums
- * carry 48 bits or more.  Where p or p - q is NaN, infinite or not positive it
+ * carry 48 bits or more (W has to stay within the range of fp32).  Where p or p - q is NaN, infinite or not positive it
  * weighs nothing; where that leaves W = 0 after a rejection the token is drawn
  * from p_A, and where that is empty too it is -1, with GDN_DEV_BAD_PROBS.  A u
  * below 0 counts as 0, one of 1 or more (or NaN) draws the last (first) token

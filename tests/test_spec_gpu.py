@@ -163,6 +163,24 @@ def test_probs_rows_past_32_bit_offsets():
     assert torch.equal(p[-1], one[0]) and bool((p[-2] == 1 / vocab).all()) and bool((p[0] == 1 / vocab).all())
 
 
+@pytest.mark.parametrize("dtype,vocab", [(BF16, 4099), (F32, 517), (BF16, 20011)])
+def test_probs_more_rows_than_fit_at_once(dtype, vocab):
+    """Clusters take several rows, in turn aligned, masked, greedy, plain or
+    left out, so that a row's state could leak into the next one's."""
+    rows = 3000 if vocab < 5000 else 1200
+    rng = np.random.default_rng(vocab)
+    x = logits_of(rows, vocab, dtype, 8)
+    x[::5] = x[::5].masked_fill(torch.rand_like(x[::5], dtype=F32) < 0.9, -float("inf"))
+    x[::11] = -float("inf")
+    x[3::17, ::3] = float("nan")
+    x[7::19, vocab // 2] = float("inf")
+    x[4::23] *= 1e6 if dtype == F32 else 2.0**20
+    temps = gpu(np.array([1, 0, 0.5, -1, 2, 0, 1], np.float32))
+    seq = gpu(rng.integers(-2, 8, rows).astype(np.int32))
+    seq[1500 % rows:1700 % rows] = -1
+    check_probs(x, torch.full((rows, vocab), 3.0, device="cuda"), temps, seq)
+
+
 # ---------------------------------------------------------------- verification
 
 def problem(n, d, vocab, dtype, seed, onehot=False, lens=None, close=0.5):
@@ -238,6 +256,18 @@ def test_verify_ragged_padded_and_bad_rows(onehot):
     p["cu_seqlens"][9] = p["cu_seqlens"][8] + 5                      # longer than D + 1, past the rows
     p["cu_seqlens"][0] = -1
     check_verify(p)
+
+
+@pytest.mark.parametrize("n,d,vocab,dtype", [(1300, 1, 1500, F32), (600, 1, 5003, BF16), (200, 2, 9000, F32), (150, 1, 12345, F32), (8, 1, 70000, BF16)])
+def test_verify_batches_of_every_cluster_size(n, d, vocab, dtype):
+    check_verify(problem(n, d, vocab, dtype, 7))
+
+
+def test_verify_with_nothing_to_judge():
+    p = problem(3, 2, 50, F32, 1, lens=[0, 0, 0])
+    assert check_verify(p).tolist() == [0, 0, 0]
+    p = problem(2, 0, 50, F32, 1)
+    check_verify({**p, "draft_probs": torch.zeros(2, 0, 50, device="cuda")})
 
 
 def test_verify_fixed_length_rows_and_strides():
@@ -528,6 +558,37 @@ def test_prepared_calls_streams_graphs_and_pdl():
         p["uniforms"].uniform_()
         graph.replay()
         check()
+
+
+def test_shapes_first_seen_in_a_capture():
+    """A graph captured from shapes that no call has run before."""
+    x, p = logits_of(77, 9123, F32, 41), torch.zeros(77, 9123, device="cuda")
+    q = problem(37, 2, 3111, F32, 42)
+    o = outputs(37, 2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        spec.token_probs(x, p)
+        spec.verify_drafts(**q, **o)
+    graph.replay()
+    check = torch.zeros_like(p)
+    spec.token_probs(x, check)
+    again = outputs(37, 2)
+    spec.verify_drafts(**q, **again)
+    assert torch.equal(p, check) and torch.equal(o["out_tokens"], again["out_tokens"])
+
+
+def test_results_do_not_change_from_run_to_run():
+    """No order of arrival enters a result: 20 runs, the same bits."""
+    x = logits_of(64, 50021, F32, 51)
+    p, first = torch.zeros_like(x), None
+    q = problem(64, 3, 10007, BF16, 52)
+    for _ in range(20):
+        o = outputs(64, 3)
+        spec.token_probs(x, p)
+        spec.verify_drafts(**q, **o)
+        got = (p.clone(), o["out_tokens"], o["num_tokens"])
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
 
 
 def test_two_verifications_at_once():
