@@ -470,14 +470,15 @@ GDN_API int gdn_step_maps(const gdn_step_maps_call *c)
     p.C = static_cast<int32_t>(C);
     p.B = c->block_tables ? static_cast<int32_t>(c->block_tables->shape[1]) : 0;
     p.F = c->free_blocks ? static_cast<int32_t>(c->free_blocks->shape[0]) : 0;
-    p.block_size = c->block_size;
-    // few requests and rows: one each a thread (128 requests, 640 rows: 3.0 us
-    // against 5.0 with four)
-    const int each = N <= 256 && C <= 65536 ? 1 : 4;
-    const int64_t tile = gdn::spec::MAPS_THREADS * each, tiles = (C + tile - 1) / tile;
-    return status_from(launch_ex(each == 1 ? gdn::spec::gdn_step_maps_kernel<1> : gdn::spec::gdn_step_maps_kernel<4>,
-                                 dim3(static_cast<unsigned>(tiles > 0 ? tiles : 1)), dim3(gdn::spec::MAPS_THREADS), 0,
-                                 stream_of(c->extra), true, p));
+    p.block_size = gdn::spec::Divisor::of(static_cast<uint32_t>(given ? c->block_size : 1));
+    // one request or row a thread where there are few
+    const bool many_requests = N > gdn::spec::MAPS_THREADS, many_rows = many_requests || C > 65536;
+    const auto kernel = many_requests ? gdn::spec::gdn_step_maps_kernel<4, 4>
+                        : many_rows   ? gdn::spec::gdn_step_maps_kernel<1, 4>
+                                      : gdn::spec::gdn_step_maps_kernel<1, 1>;
+    const int64_t tile = gdn::spec::MAPS_THREADS * (many_rows ? 4 : 1), tiles = (C + tile - 1) / tile;
+    return status_from(launch_ex(kernel, dim3(static_cast<unsigned>(tiles > 0 ? tiles : 1)),
+                                 dim3(gdn::spec::MAPS_THREADS), 0, stream_of(c->extra), true, p));
 }
 
 }  // extern "C"

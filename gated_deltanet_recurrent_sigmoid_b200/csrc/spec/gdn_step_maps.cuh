@@ -4,16 +4,34 @@
 // Two running sums over the requests (tokens, new blocks) and one row of output
 // per token.  One launch: every CTA sums all N requests for itself (a few KB
 // from L2) instead of waiting for another, marks where the requests that cross
-// its 1024 packed rows begin, and a running maximum over the marks tells each
-// row its request.  A thread takes four requests and four rows at a time, so
-// the rows' 16 bytes are written as whole words.  Bound by latency: two global
-// loads one behind the other (the request, its block), then the stores.
+// its packed rows begin, and a running maximum over the marks tells each row its
+// request.  Where there are many, a thread takes four requests or rows at a
+// time, the rows' 16 bytes then as whole words.  Bound by latency: two global
+// loads one behind the other (the request, its block) and the scans between.
 #pragma once
 
 #include "gdn_spec_common.cuh"
 
 namespace gdn {
 namespace spec {
+
+// Division by a number known on the host (Granlund and Montgomery, "Division by
+// invariant integers using multiplication"): exact for every 32-bit dividend.
+struct Divisor {
+    uint32_t by, factor, shift1, shift2;
+    static Divisor of(uint32_t d)
+    {
+        uint32_t l = 0;
+        while (l < 32 && (1ull << l) < d)
+            ++l;
+        return {d, static_cast<uint32_t>(((1ull << 32) * ((1ull << l) - d)) / d + 1), l < 1 ? l : 1, l > 1 ? l - 1 : 0};
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t n) const
+    {
+        const uint32_t t = __umulhi(factor, n);
+        return (t + ((n - t) >> shift1)) >> shift2;
+    }
+};
 
 struct MapsParams {
     const int32_t *lengths, *context, *slots;
@@ -24,7 +42,8 @@ struct MapsParams {
     int64_t *slot_map;
     uint32_t *status;
     int64_t b_row;
-    int32_t N, C, B, F, block_size, blocked;
+    int32_t N, C, B, F, blocked;
+    Divisor block_size;
 };
 
 constexpr int MAPS_THREADS = 256;
@@ -71,11 +90,11 @@ struct MapsRequest {
     int32_t seq, begin, context, held, fresh;      // fresh: where its new blocks begin in free_blocks
 };
 
-// EACH: requests of a scan step, and rows, per thread.
-template <int EACH>
+// REQS, ROWS: requests of a scan step, and rows, per thread.
+template <int REQS, int ROWS>
 __global__ void __launch_bounds__(MAPS_THREADS) gdn_step_maps_kernel(const MapsParams a)
 {
-    constexpr int TILE = MAPS_THREADS * EACH;
+    constexpr int TILE = MAPS_THREADS * ROWS, STEP = MAPS_THREADS * REQS;
     __shared__ Sums warp_sums[2][MAPS_WARPS];
     __shared__ MapsRequest mark[TILE];                // request that begins, or goes on, at this row; seq -1: none
     __shared__ int32_t warp_max[MAPS_WARPS];
@@ -91,18 +110,18 @@ __global__ void __launch_bounds__(MAPS_THREADS) gdn_step_maps_kernel(const MapsP
     if (blocks)
         head = *a.free_head;
 #pragma unroll
-    for (int e = 0; e < EACH; ++e)
+    for (int e = 0; e < ROWS; ++e)
         mark[e * MAPS_THREADS + tid].seq = -1;
     if (tid == 0)
         cut = {-1, 0};
 
     Sums base = {0, 0};
-    const int steps = (a.N + TILE - 1) / TILE;
+    const int steps = (a.N + STEP - 1) / STEP;
     for (int k = 0; k < steps; ++k) {
-        const int32_t i0 = k * TILE + tid * EACH;
-        int32_t slot[EACH], len[EACH], have[EACH], held[EACH];
+        const int32_t i0 = k * STEP + tid * REQS;
+        int32_t slot[REQS], len[REQS], have[REQS], held[REQS];
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) {
+        for (int e = 0; e < REQS; ++e) {
             const bool in = i0 + e < a.N;
             slot[e] = in ? a.slots[i0 + e] : -1;
             len[e] = in ? a.lengths[i0 + e] : 0;
@@ -114,9 +133,9 @@ __global__ void __launch_bounds__(MAPS_THREADS) gdn_step_maps_kernel(const MapsP
             room = usable ? a.F - head : -1;               // -1: nothing fits
             bad |= usable ? 0u : GDN_DEV_BAD_BLOCKS;
         }
-        Sums mine[EACH], own = {0, 0};
+        Sums mine[REQS], own = {0, 0};
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) {
+        for (int e = 0; e < REQS; ++e) {
             mine[e] = {0, 0};
             uint32_t wrong = slot[e] < -1 ? GDN_DEV_BAD_SLOT : 0u;
             if (len[e] < 0 || have[e] < 0 || static_cast<long long>(len[e]) + have[e] > INT32_MAX)
@@ -124,9 +143,8 @@ __global__ void __launch_bounds__(MAPS_THREADS) gdn_step_maps_kernel(const MapsP
             if (slot[e] != -1 && !wrong && len[e] > 0) {
                 mine[e].tok = len[e];
                 if (blocks) {
-                    const uint32_t need = (static_cast<uint32_t>(have[e]) + len[e] + a.block_size - 1) /
-                                          static_cast<uint32_t>(a.block_size);
-                    if (held[e] < 0 || held[e] > a.B || static_cast<long long>(held[e]) * a.block_size < have[e] ||
+                    const uint32_t need = a.block_size.quotient(static_cast<uint32_t>(have[e]) + len[e] + a.block_size.by - 1);
+                    if (held[e] < 0 || held[e] > a.B || static_cast<long long>(held[e]) * a.block_size.by < have[e] ||
                         need > static_cast<uint32_t>(a.B)) {
                         wrong |= GDN_DEV_BAD_BLOCKS;
                         mine[e].tok = 0;
@@ -143,10 +161,10 @@ __global__ void __launch_bounds__(MAPS_THREADS) gdn_step_maps_kernel(const MapsP
         from.add(base);
         // both sums only grow, so what fits is a run of requests from the first
         auto fits = [&](const Sums &s) { return s.tok <= a.C && (!blocks || s.blk <= room); };
-        Sums to[EACH];
+        Sums to[REQS];
         Sums at = from;
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) {
+        for (int e = 0; e < REQS; ++e) {
             const Sums prior = at;
             at.add(mine[e]);
             to[e] = at;
@@ -158,7 +176,7 @@ __global__ void __launch_bounds__(MAPS_THREADS) gdn_step_maps_kernel(const MapsP
         if (!whole)
             __syncthreads();
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) {
+        for (int e = 0; e < REQS; ++e) {
             const int32_t i = i0 + e;
             const bool in = whole || fits(to[e]), runs = mine[e].tok > 0 && in;
             const Sums prior = {to[e].tok - mine[e].tok, to[e].blk - mine[e].blk};
@@ -191,10 +209,10 @@ __global__ void __launch_bounds__(MAPS_THREADS) gdn_step_maps_kernel(const MapsP
     pdl_trigger();
 
     // ---- each row's request: the last mark at or before it
-    const int r0 = tid * EACH;
+    const int r0 = tid * ROWS;
     int32_t h = -1;
 #pragma unroll
-    for (int e = 0; e < EACH; ++e)
+    for (int e = 0; e < ROWS; ++e)
         if (mark[r0 + e].seq >= 0)
             h = r0 + e;
     __syncwarp();
@@ -216,42 +234,48 @@ __global__ void __launch_bounds__(MAPS_THREADS) gdn_step_maps_kernel(const MapsP
     const long long t0 = row0 + r0;
     if (t0 >= a.C)
         return;
-    int32_t seq[EACH], pos[EACH], block[EACH], in[EACH];
+    int32_t seq[ROWS], pos[ROWS], block[ROWS], in[ROWS];
+    int32_t *fresh[ROWS];                                  // where a new block's first token enters it, else NULL
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) {
+    for (int e = 0; e < ROWS; ++e) {
         if (mark[r0 + e].seq >= 0)
             h = r0 + e;
         seq[e] = pos[e] = block[e] = -1;
         in[e] = 0;
+        fresh[e] = nullptr;
         if (t0 + e < end.tok && h >= 0) {
             const MapsRequest q = mark[h];
             seq[e] = q.seq;
             pos[e] = q.context + static_cast<int32_t>(t0 + e - q.begin);
             if (blocks) {
-                const int32_t lb = pos[e] / a.block_size;
-                in[e] = pos[e] - lb * a.block_size;
-                block[e] = lb < q.held ? a.tables[q.seq * a.b_row + lb] : a.free_blocks[q.fresh + lb - q.held];
-                if (lb >= q.held && in[e] == 0)            // a new block's first token
-                    a.tables[q.seq * a.b_row + lb] = block[e];
+                const int32_t lb = static_cast<int32_t>(a.block_size.quotient(pos[e]));
+                int32_t *const entry = a.tables + q.seq * a.b_row + lb;
+                in[e] = pos[e] - lb * static_cast<int32_t>(a.block_size.by);
+                block[e] = lb < q.held ? *entry : a.free_blocks[q.fresh + lb - q.held];
+                fresh[e] = lb >= q.held && in[e] == 0 ? entry : nullptr;
             }
         }
     }
-    long long place[EACH];
+    // (stores behind all loads: they might alias for all the compiler knows)
+    long long place[ROWS];
 #pragma unroll
-    for (int e = 0; e < EACH; ++e)
-        place[e] = seq[e] >= 0 ? static_cast<long long>(block[e]) * a.block_size + in[e] : -1;
+    for (int e = 0; e < ROWS; ++e) {
+        place[e] = seq[e] >= 0 ? static_cast<long long>(block[e]) * a.block_size.by + in[e] : -1;
+        if (fresh[e])
+            *fresh[e] = block[e];
+    }
     const uintptr_t lie = reinterpret_cast<uintptr_t>(a.row_seq) | reinterpret_cast<uintptr_t>(a.positions) |
                           reinterpret_cast<uintptr_t>(a.slot_map);
-    if (EACH == 4 && t0 + EACH <= a.C && (lie & 15u) == 0) {
-        *reinterpret_cast<int4 *>(a.row_seq + t0) = make_int4(seq[0], seq[1 % EACH], seq[2 % EACH], seq[3 % EACH]);
-        *reinterpret_cast<int4 *>(a.positions + t0) = make_int4(pos[0], pos[1 % EACH], pos[2 % EACH], pos[3 % EACH]);
+    if (ROWS == 4 && t0 + ROWS <= a.C && (lie & 15u) == 0) {
+        *reinterpret_cast<int4 *>(a.row_seq + t0) = make_int4(seq[0], seq[1 % ROWS], seq[2 % ROWS], seq[3 % ROWS]);
+        *reinterpret_cast<int4 *>(a.positions + t0) = make_int4(pos[0], pos[1 % ROWS], pos[2 % ROWS], pos[3 % ROWS]);
         if (blocks) {
-            *reinterpret_cast<longlong2 *>(a.slot_map + t0) = make_longlong2(place[0], place[1 % EACH]);
-            *reinterpret_cast<longlong2 *>(a.slot_map + t0 + 2) = make_longlong2(place[2 % EACH], place[3 % EACH]);
+            *reinterpret_cast<longlong2 *>(a.slot_map + t0) = make_longlong2(place[0], place[1 % ROWS]);
+            *reinterpret_cast<longlong2 *>(a.slot_map + t0 + 2) = make_longlong2(place[2 % ROWS], place[3 % ROWS]);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < EACH; ++e)
+        for (int e = 0; e < ROWS; ++e)
             if (t0 + e < a.C) {
                 a.row_seq[t0 + e] = seq[e];
                 a.positions[t0 + e] = pos[e];

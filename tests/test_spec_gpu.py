@@ -458,7 +458,8 @@ def check_maps(p, capacity, row_stride=0, **more):
 
 @pytest.mark.parametrize("blocks", [False, True])
 @pytest.mark.parametrize("n,longest,cached,block", [(1, 1, 0, 1), (1, 5000, 3, 7), (2, 3, 100, 16), (33, 40, 64, 16), (128, 4, 3000, 64),
-                                                    (1023, 9, 500, 24), (1025, 3, 10, 1), (2500, 2, 40, 128), (7, 3000, 9000, 100)])
+                                                    (1023, 9, 500, 24), (1025, 3, 10, 1), (2500, 2, 40, 128), (7, 3000, 9000, 100), (60, 4000, 5000, 64),
+                                                    (257, 700, 100, 48)])
 def test_maps(n, longest, cached, block, blocks):
     p, capacity = maps_problem(n, longest, cached, block, n, blocks=blocks)
     check_maps(p, capacity, row_stride=3)
