@@ -2,7 +2,10 @@
 // its slot of the pool (gdn_commit_states in include/gdn_spec.h).
 //
 // A copy of K V fp32 values per (sequence, head): bound by HBM, each byte read
-// once and written once.
+// once and written once.  128 sequences x 8 heads in 22.6 us (5.9 TB/s, 0.92 of
+// the measured copy rate), 486 x 8 in 80 us (0.99).  CTAs of 8 KB; 4, 16 and 32
+// KB are within 2 % (a few states want the smaller ones: 4 x 4 in 1.6 us against
+// 2.1 with 32 KB).
 #pragma once
 
 #include "gdn_spec_common.cuh"

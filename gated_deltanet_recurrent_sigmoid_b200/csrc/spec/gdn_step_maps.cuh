@@ -7,7 +7,9 @@
 // its packed rows begin, and a running maximum over the marks tells each row its
 // request.  Where there are many, a thread takes four requests or rows at a
 // time, the rows' 16 bytes then as whole words.  Bound by latency: two global
-// loads one behind the other (the request, its block) and the scans between.
+// loads one behind the other (the request, its block) and the scans between:
+// 128 requests and 640 rows in 2.5 us, 1024 requests and 34,000 rows in 4.4,
+// 96 requests and 205,000 rows in 3.8 (5.4 with four requests a thread).
 #pragma once
 
 #include "gdn_spec_common.cuh"

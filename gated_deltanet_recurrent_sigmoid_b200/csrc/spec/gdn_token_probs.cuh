@@ -9,7 +9,13 @@
 // rather than kept.  Each of the first two ends in one exchange over
 // distributed shared memory.  What a row needs besides its logits is loaded a
 // row ahead.
-// Bound by HBM: each logit read once, each probability written once.
+// Bound by HBM: each logit read once, each probability written once.  512 x
+// 131072 bf16 -> fp32 in 73 us, 5.5 TB/s, 0.85 of the measured copy rate; fp32
+// -> fp32 in 102 us (0.81: the slice takes twice the shared memory, three CTAs
+// an SM instead of six keep copies in flight); bf16 -> bf16 in 61 us (0.68: the
+// two powers a logit and the issue slots begin to count).  A single row of
+// 32768 takes 3.7 us, all of it latency.  CTAs of 512 threads, fewer of them
+// resident, took 84 us; one pass with a running maximum and sum 116.
 #pragma once
 
 #include "gdn_spec_common.cuh"
