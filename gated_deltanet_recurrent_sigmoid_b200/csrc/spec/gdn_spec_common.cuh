@@ -26,7 +26,8 @@ __device__ __forceinline__ void report(uint32_t *status, uint32_t bits)
         atomicOr(status, bits);
 }
 
-// This thread's warp, the same register for the whole warp.  Branches on it are
+// This thread's warp, the same register for the whole warp.  A shuffle: every
+// lane has to call it.  Branches on it are
 // then known to be uniform: shuffles behind a branch or loop that might be
 // divergent are compiled to a path of about 230 clocks each instead of 24
 // (measured), which __syncwarp() behind a loop avoids as well.
