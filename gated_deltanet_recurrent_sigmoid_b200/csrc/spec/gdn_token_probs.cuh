@@ -10,9 +10,9 @@
 // distributed shared memory.  What a row needs besides its logits is loaded a
 // row ahead.
 // Bound by HBM: each logit read once, each probability written once.  512 x
-// 131072 bf16 -> fp32 in 73 us, 5.5 TB/s, 0.85 of the measured copy rate; fp32
-// -> fp32 in 102 us (0.81: the slice takes twice the shared memory, three CTAs
-// an SM instead of six keep copies in flight); bf16 -> bf16 in 61 us (0.68: the
+// 131072 bf16 -> fp32 in 70 us, 5.8 TB/s, 0.89 of the measured copy rate; fp32
+// -> fp32 in 97 us (0.86: the slice takes twice the shared memory, three CTAs
+// an SM instead of six keep copies in flight); bf16 -> bf16 in 59 us (0.71: the
 // two powers a logit and the issue slots begin to count).  A single row of
 // 32768 takes 3.7 us, all of it latency.  CTAs of 512 threads, fewer of them
 // resident, took 84 us; one pass with a running maximum and sum 116.
@@ -37,7 +37,10 @@ struct ProbsParams {
 };
 
 constexpr int PROBS_MAX_THREADS = 256;
-constexpr int PROBS_PIECE = 8192;                          // bytes per bulk copy and mbarrier
+// Bytes per bulk copy and mbarrier.  (8 KB pieces, whose maxima overlap the
+// copies of the later ones: 1 % slower throughout, one row of 131072 5.5 us
+// against 5.2.)
+constexpr int PROBS_PIECE = 32768;
 constexpr int PROBS_MAX_SLICE_BYTES = GDN_SPEC_MAX_VOCAB / 8 * 4;
 constexpr int PROBS_MAX_PIECES = PROBS_MAX_SLICE_BYTES / PROBS_PIECE + 2;
 constexpr int PROBS_MAX_CLUSTER = 8;
@@ -179,7 +182,7 @@ __device__ __forceinline__ void write_row(const TIn *el, TOut *dst, int32_t n, V
     };
     constexpr int GROUP_BYTES = PO * sizeof(TIn);                    // 8, 16 or 32
     if (sync::smem_addr(from) % (GROUP_BYTES < 16 ? GROUP_BYTES : 16) == 0) {
-#pragma unroll 2
+#pragma unroll 4
         for (int g = tid; g < groups; g += threads) {
             float x[PO];
             load_group(from + g * PO, x);
