@@ -56,7 +56,6 @@ __global__ void __launch_bounds__(COMMIT_THREADS) gdn_commit_states_kernel(const
 #pragma unroll
     for (int k = 0; k < COMMIT_VECS; ++k)
         __stcs(dst + at + k * COMMIT_THREADS, v[k]);
-    pdl_trigger();
 }
 
 }  // namespace spec

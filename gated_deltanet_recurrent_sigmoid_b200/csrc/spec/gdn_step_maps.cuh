@@ -8,8 +8,8 @@
 // request.  Where there are many, a thread takes four requests or rows at a
 // time, the rows' 16 bytes then as whole words.  Bound by latency: two global
 // loads one behind the other (the request, its block) and the scans between:
-// 128 requests and 640 rows in 2.5 us, 1024 requests and 34,000 rows in 4.4,
-// 96 requests and 205,000 rows in 3.8 (5.4 with four requests a thread).
+// 128 requests and 640 rows in 2.7 us, 1024 requests and 34,000 rows in 4.6,
+// 96 requests and 205,000 rows in 3.9 (5.4 with four requests a thread).
 #pragma once
 
 #include "gdn_spec_common.cuh"
@@ -208,7 +208,6 @@ __global__ void __launch_bounds__(MAPS_THREADS) gdn_step_maps_kernel(const MapsP
         if (bad)
             report(a.status, bad);
     }
-    pdl_trigger();
 
     // ---- each row's request: the last mark at or before it
     const int r0 = tid * ROWS;

@@ -11,8 +11,8 @@
 // row ahead.
 // Bound by HBM: each logit read once, each probability written once.  512 x
 // 131072 bf16 -> fp32 in 70 us, 5.8 TB/s, 0.89 of the measured copy rate; fp32
-// -> fp32 in 97 us (0.86: the slice takes twice the shared memory, three CTAs
-// an SM instead of six keep copies in flight); bf16 -> bf16 in 59 us (0.71: the
+// -> fp32 in 94 us (0.88: the slice takes twice the shared memory, three CTAs
+// an SM instead of six keep copies in flight); bf16 -> bf16 in 57 us (0.72: the
 // two powers a logit and the issue slots begin to count).  A single row of
 // 32768 takes 3.7 us, all of it latency.  CTAs of 512 threads, fewer of them
 // resident, took 84 us; one pass with a running maximum and sum 116.
@@ -315,8 +315,6 @@ __global__ void __launch_bounds__(PROBS_MAX_THREADS, 6) gdn_token_probs_kernel(c
                     inv = 1.f / over_cluster<Sum>(s, sh, exchange, rank, size);
                 }
             }
-            if (next >= p.rows)
-                pdl_trigger();
             failed = sh.failed;                            // (the same in the CTA behind an exchange)
             if (!failed) {
                 TOut *const dst = static_cast<TOut *>(p.probs) + row * p.p_row + e0;

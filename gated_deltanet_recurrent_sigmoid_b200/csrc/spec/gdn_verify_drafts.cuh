@@ -525,7 +525,6 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
             }
             return;
         }
-        pdl_trigger();
         if (segment / warps != static_cast<int>(rank))
             return;
 
