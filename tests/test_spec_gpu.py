@@ -609,6 +609,73 @@ def test_two_verifications_at_once():
         assert torch.equal(o["out_tokens"], again["out_tokens"]) and torch.equal(o["num_tokens"], again["num_tokens"])
 
 
+def test_two_captured_graphs_at_once():
+    """Replays of two graphs that overlap on two streams share nothing."""
+    sets = []
+    for seed in (61, 62):
+        x, q = logits_of(300, 20011, F32, seed), problem(90, 2, 20011, F32, seed)
+        p, o = torch.zeros(300, 20011, device="cuda"), outputs(90, 2)
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=stream):
+            spec.token_probs(x, p)
+            spec.verify_drafts(**q, **o)
+        sets.append((x, q, p, o, graph, stream))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for *_, graph, stream in sets:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for x, q, p, o, *_ in sets:
+        check, again = torch.zeros_like(p), outputs(90, 2)
+        spec.token_probs(x, check)
+        spec.verify_drafts(**q, **again)
+        assert torch.equal(p, check) and torch.equal(o["out_tokens"], again["out_tokens"])
+
+
+def test_first_calls_from_several_threads():
+    """A fresh process whose first calls of each kernel come from six threads
+    at once (one-time set-up per device, the remembered launch shapes)."""
+    code = """
+import sys, threading
+sys.path[:0] = [{root!r}]
+import torch
+from gated_deltanet_recurrent_sigmoid_b200 import speculative as spec
+spec.load()
+jobs, errors, start = [], [], threading.Barrier(6)
+for k in range(6):
+    vocab = (1000, 40000, 131072)[k % 3]
+    x = torch.randn(20, vocab, device="cuda").to((torch.float32, torch.bfloat16)[k % 2])
+    jobs.append((x, torch.zeros(20, vocab, device="cuda"), torch.zeros(20, 1, dtype=torch.int32, device="cuda"),
+                 torch.zeros(20, dtype=torch.int32, device="cuda"), torch.full((20, 1), 0.5, device="cuda"), torch.cuda.Stream()))
+torch.cuda.synchronize()
+def run(job):
+    x, p, out, num, u, stream = job
+    try:
+        start.wait()
+        for _ in range(20):
+            spec.token_probs(x, p, stream=stream)
+            spec.verify_drafts(p[:, None], torch.zeros(20, 0, dtype=torch.int32, device="cuda"), None, u, out, num, stream=stream)
+        stream.synchronize()
+    except Exception as e:
+        errors.append(repr(e))
+threads = [threading.Thread(target=run, args=(j,)) for j in jobs]
+for t in threads: t.start()
+for t in threads: t.join()
+assert not errors, errors
+for x, p, out, num, u, stream in jobs:
+    assert torch.allclose(p, torch.softmax(x.double(), -1).float(), atol=1e-6)
+    below = p.double().cumsum(-1)
+    want = (below > 0.5 * below[:, -1:]).int().argmax(-1)
+    assert torch.equal(out[:, 0].long(), want) and bool((num == 1).all())
+print("threads agree")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "threads agree" in r.stdout, r.stderr[-2000:]
+
+
 def test_host_tensors_are_refused():
     with pytest.raises(ValueError):
         spec.token_probs(torch.zeros(1, 8), torch.zeros(1, 8, device="cuda"))
