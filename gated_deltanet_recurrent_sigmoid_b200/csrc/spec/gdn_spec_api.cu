@@ -124,9 +124,12 @@ cudaError_t launch_probs(const gdn::spec::ProbsParams &p, int64_t rows, int clus
     cudaError_t err = cudaGetDevice(&dev);
     if (err == cudaSuccess)
         err = once_per_device(once, dev, [&]() {
-            return cudaFuncSetAttribute(gdn::spec::gdn_token_probs_kernel<TIn, TOut>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(gdn::spec::probs_smem(gdn::spec::PROBS_MAX_SLICE_BYTES)));
+            const auto kernel = gdn::spec::gdn_token_probs_kernel<TIn, TOut>;
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(gdn::spec::probs_smem(gdn::spec::PROBS_MAX_SLICE_BYTES)));
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            return e;
         });
     // The clusters that fit the GPU at once, for the last launch shape asked
     // for on each device: shape in the upper half, clusters in the lower.
@@ -154,12 +157,16 @@ cudaError_t launch_probs(const gdn::spec::ProbsParams &p, int64_t rows, int clus
 // give them, and more CTAs while the grid leaves SMs idle and a slice keeps
 // 1024 elements.  Measured for 512 rows bf16 -> fp32: 4096 logits in 1 CTA 5.8
 // us, in 4 8.5; 32768 in 1 28.8, in 4 22.0, in 8 25.2; 50021 fp32 in 4 43.5, in
-// 8 41.0.
+// 8 41.0.  16 CTAs where 8 would leave a slice over 32 KB, or SMs idle (131072
+// fp32 in 8 94 us, in 16 91; bf16 in 8 69, in 16 72; one row of it in 8 5.3, in
+// 16 4.4).
 int probs_cluster(int64_t rows, int64_t row_bytes, int64_t vocab, int sms)
 {
     int c = 1;
     while (c < 8 && (row_bytes > c * 16384ll || (rows * c < sms && vocab > c * 1024ll)))
         c *= 2;
+    if (c == 8 && (row_bytes > 8 * 32768ll || (rows * 16 <= sms && vocab > 16 * 1024ll)))
+        c = 16;
     return c;
 }
 

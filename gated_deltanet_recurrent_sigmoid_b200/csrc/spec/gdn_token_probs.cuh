@@ -11,9 +11,8 @@
 // row ahead.
 // Bound by HBM: each logit read once, each probability written once.  512 x
 // 131072 bf16 -> fp32 in 70 us, 5.8 TB/s, 0.89 of the measured copy rate; fp32
-// -> fp32 in 94 us (0.88: the slice takes twice the shared memory, three CTAs
-// an SM instead of six keep copies in flight); bf16 -> bf16 in 57 us (0.72: the
-// two powers a logit and the issue slots begin to count).  A single row of
+// -> fp32 in 91 us (0.91); bf16 -> bf16 in 57 us (0.72: the two powers a logit
+// and the issue slots begin to count).  A single row of
 // 32768 takes 3.7 us, all of it latency.  CTAs of 512 threads, fewer of them
 // resident, took 84 us; one pass with a running maximum and sum 116.
 #pragma once
@@ -41,9 +40,9 @@ constexpr int PROBS_MAX_THREADS = 256;
 // copies of the later ones: 1 % slower throughout, one row of 131072 5.5 us
 // against 5.2.)
 constexpr int PROBS_PIECE = 32768;
-constexpr int PROBS_MAX_SLICE_BYTES = GDN_SPEC_MAX_VOCAB / 8 * 4;
+constexpr int PROBS_MAX_CLUSTER = 16;
+constexpr int PROBS_MAX_SLICE_BYTES = GDN_SPEC_MAX_VOCAB / PROBS_MAX_CLUSTER * 4;
 constexpr int PROBS_MAX_PIECES = PROBS_MAX_SLICE_BYTES / PROBS_PIECE + 2;
-constexpr int PROBS_MAX_CLUSTER = 8;
 
 struct ProbsShared {
     float cta[2][PROBS_MAX_CLUSTER];                       // one value of each CTA of the cluster; exchanges alternate
