@@ -113,10 +113,10 @@ __device__ __forceinline__ void st_peer(uint32_t addr, float x, uint32_t bar)
                  "r"(__float_as_uint(x)), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ void st_peer(uint32_t addr, float x, float y, uint32_t bar)
+__device__ __forceinline__ void st_peer(uint32_t addr, double x, uint32_t bar)
 {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(addr),
-                 "r"(__float_as_uint(x)), "r"(__float_as_uint(y)), "r"(bar)
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(addr),
+                 "l"(__double_as_longlong(x)), "r"(bar)
                  : "memory");
 }
 

@@ -7,18 +7,18 @@
 // cross the cluster through distributed shared memory; every CTA then knows W
 // and which segment holds the first v with w_0 + ... + w_v > u W, and the CTA
 // that owns it goes through that one segment again (from L2).  The order of all
-// sums is fixed by the sizes alone.
+// sums is fixed by the arguments (sizes, alignment, values), not by timing.
 //
-// The token must not depend on that order, so a sum keeps what its additions
-// round off: it is a pair (s, c) of fp32 values, s the rounded sum and c the
-// exact errors of its additions (and of p - q) added up, good to about 2^-48.
-// An addition is 7 fp32 operations at 128 a clock and SM; one in fp64 would
-// need 2 conversions (4 with q) at 16 a clock beside it.
+// The token must not depend on that order, so every sum is fp64: rows whose
+// weights are multiples of 2^-52 of their total are summed exactly.  An
+// addition is a conversion (two with q) and an fp64 operation, both at a
+// fraction of the fp32 rate and still faster than pairs of fp32, 7 operations
+// an element, which keep 36 to 47 bits.
 // Bound by HBM while the rows stream: one row of p, one of q at a rejection.
-// 128 sequences x 131072 fp32, a third of them rejected: 24 us (3.7 TB/s; the
+// 128 sequences x 131072 fp32, a third of them rejected: 22.7 us (3.9 TB/s; the
 // 67 MB of p alone stream in 11 us), of which about 2 pass before the rows are
 // known, 4 in the exchange and the second reading, and the rest waits for the
-// sequences that need q too.  One sequence of 32768: 5.5 us of latency.
+// sequences that need q too.  One sequence of 32768: 5.3 us of latency.
 #pragma once
 
 #include "gdn_spec_common.cuh"
@@ -53,126 +53,65 @@ enum class Less { none, row, token };
 // A positive finite number (or +0).
 __device__ __forceinline__ bool counts(float x) { return __float_as_uint(x) < 0x7f800000u; }
 
-// A sum that keeps its rounding errors: s + c.
-struct PairSum {
-    float s = 0.f, c = 0.f;
-    __device__ __forceinline__ void add(float x)
-    {
-        const float t = s + x, b = t - s;
-        c += (s - (t - b)) + (x - b);                // s + x = t + this, exactly
-        s = t;
+// A token's weight in 64 bits: p, or p - q (exact unless their exponents lie
+// further apart than 64 bits hold).
+template <bool ROW>
+__device__ __forceinline__ double weight(float p, float q, bool in)
+{
+    if (ROW) {
+        in = in && fabsf(p) < INFINITY && fabsf(q) < INFINITY;
+        p = in ? p : 0.f;
+        q = in ? fminf(q, p) : 0.f;
+        return static_cast<double>(p) - static_cast<double>(q);
     }
-    __device__ __forceinline__ void add(const PairSum &x)
+    return static_cast<double>(in && counts(p) ? p : 0.f);
+}
+
+// A finite x >= 0 as a double, times UNIT.  fp32 by the conversion
+// instruction.  Values that were bf16 by moving the bits of exponent and
+// fraction to their places, which scales by 2^-896 (exactly, subnormals too)
+// and takes two shifts of full rate where the instruction has a quarter of it.
+// 128 x 131072: fp32 22.7 us, by shifts 25.0; bf16 15.6, by instruction 16.7.
+template <typename T> struct Wide;
+template <> struct Wide<float> {
+    static constexpr double UNIT = 1.;
+    __device__ static double of(float x) { return static_cast<double>(x); }
+};
+template <> struct Wide<__nv_bfloat16> {
+    static constexpr double UNIT = 0x1p-896;
+    __device__ static double of(float x)
     {
-        add(x.s);
-        c += x.c;
-    }
-    // The weight of a token: p, or p - q.
-    template <bool ROW>
-    __device__ __forceinline__ void weight(float p, float q, bool in)
-    {
-        if (ROW) {
-            const float d = p - q, e = (p - d) - q;  // p - q = d + e, exactly (0 <= q < p)
-            in = in && counts(d);
-            add(in ? d : 0.f);
-            c += in ? e : 0.f;
-        } else {
-            add(in && counts(p) ? p : 0.f);
-        }
-    }
-    __device__ __forceinline__ bool positive() const { return s + c > 0.f; }
-    // Whether this + x > goal.
-    __device__ __forceinline__ bool passes(const PairSum &x, const PairSum &goal) const
-    {
-        PairSum d = *this;
-        d.add(x);
-        d.add(PairSum{-goal.s, -goal.c});
-        return d.s + d.c > 0.f;
-    }
-    __device__ __forceinline__ PairSum times(float u) const
-    {
-        const float x = u * s;
-        return PairSum{x, fmaf(u, s, -x) + u * c};
+        const uint32_t b = __float_as_uint(x);
+        return __hiloint2double(static_cast<int>(b >> 3), static_cast<int>(b << 29));
     }
 };
 
-// Two such sums side by side, for p (and q) known to be finite and not
-// negative, q <= infinity.  For p alone in packed fp32 operations, one
-// instruction for both sums; with q those were slower (128 x 131072 fp32 28.8
-// us against 24.4).
-template <bool ROW>
-struct PairSum2 {
-    PairSum a, b;
+// Two sums side by side, for p (and q) known to be finite and not negative.
+template <bool ROW, typename T>
+struct WordSum {
+    double a = 0., b = 0.;
     // A q above p counts as p.
-    static __device__ __forceinline__ void add_less(PairSum &s, float p, float q)
+    static __device__ __forceinline__ double of(float p, float q)
     {
-        q = fminf(q, p);
-        const float d = p - q;
-        s.add(d);
-        s.c += (p - d) - q;
+        return ROW ? Wide<T>::of(p) - Wide<T>::of(fminf(q, p)) : Wide<T>::of(p);
     }
     __device__ __forceinline__ void add(float p0, float p1, float q0, float q1)
     {
-        add_less(a, p0, q0);
-        add_less(b, p1, q1);
+        a += of(p0, q0);
+        b += of(p1, q1);
     }
-    __device__ __forceinline__ PairSum sum() const
-    {
-        PairSum x = a;
-        x.add(b);
-        return x;
-    }
-};
-template <>
-struct PairSum2<false> {
-    uint64_t s = 0, c = 0;
-    static __device__ __forceinline__ uint64_t plus(uint64_t x, uint64_t y)
-    {
-        uint64_t r;
-        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-        return r;
-    }
-    static __device__ __forceinline__ uint64_t minus(uint64_t x, uint64_t y)   // x - y as y * -1 + x, rounded once
-    {
-        uint64_t r;
-        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(y), "l"(0xbf800000bf800000ull), "l"(x));
-        return r;
-    }
-    __device__ __forceinline__ void add(float p0, float p1, float, float)
-    {
-        uint64_t x;
-        asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(p0), "f"(p1));
-        const uint64_t t = plus(s, x), b = minus(t, s);
-        c = plus(c, plus(minus(s, minus(t, b)), minus(x, b)));
-        s = t;
-    }
-    __device__ __forceinline__ PairSum sum() const
-    {
-        PairSum x, y;
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(x.s), "=f"(y.s) : "l"(s));
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(x.c), "=f"(y.c) : "l"(c));
-        x.add(y);
-        return x;
-    }
+    __device__ __forceinline__ double sum() const { return (a + b) * (1. / Wide<T>::UNIT); }
 };
 
-__device__ __forceinline__ PairSum shfl(const PairSum &x, int from)
-{
-    return PairSum{__shfl_sync(~0u, x.s, from), __shfl_sync(~0u, x.c, from)};
-}
-__device__ __forceinline__ PairSum shfl_up(const PairSum &x, int by)
-{
-    return PairSum{__shfl_up_sync(~0u, x.s, by), __shfl_up_sync(~0u, x.c, by)};
-}
 // Sums over the lanes up to this one.
-__device__ __forceinline__ PairSum warp_upto(PairSum x)
+__device__ __forceinline__ double warp_upto(double x)
 {
     const int lane = threadIdx.x & 31;
     __syncwarp();
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const PairSum b = shfl_up(x, o);
-        x.add(lane >= o ? b : PairSum{});
+        const double b = __shfl_up_sync(~0u, x, o);
+        x += lane >= o ? b : 0.;
     }
     return x;
 }
@@ -191,19 +130,11 @@ struct Weights {
     const T *p, *q;
     int32_t out;
     template <bool ROW>
-    __device__ __forceinline__ void add_to(PairSum &s, int64_t v) const
+    __device__ __forceinline__ double at(int64_t v) const
     {
-        s.weight<ROW>(Elem<T>::get(p[v]), ROW ? Elem<T>::get(q[v]) : 0.f, ROW || v != out);
+        return weight<ROW>(Elem<T>::get(p[v]), ROW ? Elem<T>::get(q[v]) : 0.f, ROW || v != out);
     }
-    __device__ __forceinline__ PairSum at(int64_t v) const
-    {
-        PairSum s;
-        if (q)
-            add_to<true>(s, v);
-        else
-            add_to<false>(s, v);
-        return s;
-    }
+    __device__ __forceinline__ double any_at(int64_t v) const { return q ? at<true>(v) : at<false>(v); }
 };
 
 // U words of the row, at v, v + step, ...
@@ -233,7 +164,7 @@ struct Words {
     }
     // Word k added without a look at its values; the largest bit patterns say
     // afterwards whether they were finite and not negative.
-    __device__ __forceinline__ void add_valid(PairSum2<ROW> &s, uint32_t &most, int k) const
+    __device__ __forceinline__ void add_valid(WordSum<ROW, T> &s, uint32_t &most, int k) const
     {
         float pf[E], qf[E];
         unpack16(p[k], pf, static_cast<const T *>(nullptr));
@@ -247,7 +178,7 @@ struct Words {
             s.add(pf[j], pf[j + 1], ROW ? qf[j] : 0.f, ROW ? qf[j + 1] : 0.f);
     }
     // Word k, whose first element is v.
-    __device__ __forceinline__ void add_to(PairSum (&s)[2], const Weights<T> &w, int32_t v, int k) const
+    __device__ __forceinline__ void add_to(double (&s)[2], const Weights<T> &w, int32_t v, int k) const
     {
         float pf[E], qf[E];
         unpack16(p[k], pf, static_cast<const T *>(nullptr));
@@ -255,7 +186,7 @@ struct Words {
             unpack16(q[ROW ? k : 0], qf, static_cast<const T *>(nullptr));
 #pragma unroll
         for (int j = 0; j < E; ++j)
-            s[j & 1].template weight<ROW>(pf[j], ROW ? qf[j] : 0.f, ROW || v + j != w.out);
+            s[j & 1] += weight<ROW>(pf[j], ROW ? qf[j] : 0.f, ROW || v + j != w.out);
     }
 };
 
@@ -272,12 +203,12 @@ __device__ __forceinline__ bool alike(const Weights<T> &w)
 // their words, or hold values that weigh nothing whatever the other row says
 // (NaN, infinities, negative ones), every 32nd element with a look at each.
 template <bool ROW, typename T>
-__device__ __forceinline__ PairSum lane_sum(const Weights<T> &w, int32_t v0, int32_t v1, int32_t skew)
+__device__ __forceinline__ double lane_sum(const Weights<T> &w, int32_t v0, int32_t v1, int32_t skew)
 {
     constexpr int E = Elem<T>::PER16, U = 4;             // elements a word, words in flight a lane
     const int lane = threadIdx.x & 31;
     if (alike<ROW>(w)) {
-        PairSum2<ROW> pairs;
+        WordSum<ROW, T> words;
         uint32_t most = 0;
         const int32_t lead = (E - (v0 + skew) % E) % E, first = v0 + lead;   // elements before the first whole word
         const int32_t last = v1 - (v1 + skew) % E;       // the first element behind the last whole word
@@ -287,42 +218,42 @@ __device__ __forceinline__ PairSum lane_sum(const Weights<T> &w, int32_t v0, int
             x.load(w, v + lane * E, 32 * E);
 #pragma unroll
             for (int k = 0; k < U; ++k)
-                x.add_valid(pairs, most, k);
+                x.add_valid(words, most, k);
         }
         if (v < last) {
             x.load_before(w, v + lane * E, 32 * E, last);
 #pragma unroll
             for (int k = 0; k < U; ++k)
                 if (v + 32 * E * k < last)
-                    x.add_valid(pairs, most, k);
+                    x.add_valid(words, most, k);
         }
-        PairSum s = pairs.sum();
+        double s = words.sum();
         if (lane < lead && v0 + lane < v1)
-            w.template add_to<ROW>(s, v0 + lane);
+            s += w.template at<ROW>(v0 + lane);
         if (last >= first && last + lane < v1)
-            w.template add_to<ROW>(s, last + lane);
+            s += w.template at<ROW>(last + lane);
         __syncwarp();
         if (!__any_sync(~0u, beyond_finite(most, static_cast<const T *>(nullptr))))
             return s;
     }
-    PairSum s;
+    double s = 0.;
 #pragma unroll 8
     for (int32_t v = v0 + lane; v < v1; v += 32)
-        w.template add_to<ROW>(s, v);
+        s += w.template at<ROW>(v);
     return s;
 }
 
 // The sum over [v0, v1) by one thread, in the row's words as above.
 template <bool ROW, typename T>
-__device__ __forceinline__ PairSum run_sum(const Weights<T> &w, int32_t v0, int32_t v1, int32_t skew)
+__device__ __forceinline__ double run_sum(const Weights<T> &w, int32_t v0, int32_t v1, int32_t skew)
 {
     constexpr int E = Elem<T>::PER16, U = ROW ? 4 : 8;
-    PairSum s[2];
+    double s[2] = {0., 0.};
     int32_t v = v0;
     if (alike<ROW>(w)) {
         const int32_t lead = min((E - (v0 + skew) % E) % E, max(v1 - v0, 0));
         for (int32_t j = 0; j < lead; ++j)
-            w.template add_to<ROW>(s[0], v0 + j);
+            s[0] += w.template at<ROW>(v0 + j);
         for (v += lead; v + E <= v1; v += E * U) {
             Words<ROW, U, T> x;
             x.load_before(w, v, E, v1);
@@ -335,17 +266,16 @@ __device__ __forceinline__ PairSum run_sum(const Weights<T> &w, int32_t v0, int3
     }
 #pragma unroll 4
     for (; v < v1; ++v)
-        w.template add_to<ROW>(s[0], v);
-    s[0].add(s[1]);
-    return s[0];
+        s[0] += w.template at<ROW>(v);
+    return s[0] + s[1];
 }
 
 template <typename T>
 __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kernel(const VerifyParams a)
 {
-    __shared__ PairSum part[2][VERIFY_MAX_SEGS];      // segment sums of the cluster, for either attempt
-    __shared__ PairSum scan[VERIFY_MAX_WARPS];
-    __shared__ PairSum goal_at[2];                   // u W, and the sum before the chosen segment
+    __shared__ double part[2][VERIFY_MAX_SEGS];       // segment sums of the cluster, for either attempt
+    __shared__ double scan[VERIFY_MAX_WARPS];
+    __shared__ double goal_at[2];                    // u W, and the sum before the chosen segment
     __shared__ unsigned long long got[2];            // the cluster's segment sums are in
     __shared__ int chosen, first_over, last_positive, failed;
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_index(), threads = blockDim.x, warps = threads >> 5;
@@ -356,7 +286,7 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
         failed = 0;
         for (int k = 0; k < 2; ++k) {
             sync::mbar_init(&got[k], 1);
-            sync::mbar_arrive_expect_tx(&got[k], static_cast<uint32_t>(warps) * size * sizeof(PairSum));
+            sync::mbar_arrive_expect_tx(&got[k], static_cast<uint32_t>(warps) * size * sizeof(double));
         }
         sync::fence_barrier_init();
     }
@@ -444,13 +374,13 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
     };
     const int32_t v0 = begin_of(mine), v1 = begin_of(mine + 1);
     for (int attempt = 0; attempt < 2; ++attempt) {
-        PairSum sum;
+        double sum = 0.;
         if (w.q) {
             sum = lane_sum<true>(w, v0, v1, skew);
         } else {                                      // around the token that weighs nothing
             const bool cut = w.out >= v0 && w.out < v1;
             for (int32_t from = v0, to = cut ? w.out : v1;; from = to + 1, to = v1) {
-                sum.add(lane_sum<false>(w, from, to, skew));
+                sum += lane_sum<false>(w, from, to, skew);
                 if (to == v1)
                     break;
             }
@@ -458,11 +388,11 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
         __syncwarp();
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
-            sum.add(PairSum{__shfl_xor_sync(~0u, sum.s, o), __shfl_xor_sync(~0u, sum.c, o)});
+            sum += __shfl_xor_sync(~0u, sum, o);
         if (attempt == 0)
             cluster_wait();                           // every CTA's mbarriers are there
         if (lane < static_cast<int>(size))
-            st_peer(peer_addr(&part[attempt][mine], lane), sum.s, sum.c, peer_addr(&got[attempt], lane));
+            st_peer(peer_addr(&part[attempt][mine], lane), sum, peer_addr(&got[attempt], lane));
 
         // ---- where the running sum passes u W: each lane of the first warp
         // takes a run of `per` segments
@@ -470,35 +400,35 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
             const bool in = mbar_wait_peers(&got[attempt], 0);
             __syncwarp();
             const int per = (segs + 31) / 32, k0 = lane * per, k1 = min(k0 + per, segs);
-            PairSum own;
+            double own = 0.;
             for (int k = k0; k < k1; ++k)
-                own.add(part[attempt][k]);
-            const PairSum upto = warp_upto(own), goal = shfl(upto, 31).times(u);
+                own += part[attempt][k];
+            const double upto = warp_upto(own), goal = __shfl_sync(~0u, upto, 31) * u;
             // the first segment of positive weight past the goal, else the last
             // of positive weight
             int past = segs, last = -1;
-            PairSum base = shfl_up(upto, 1);
+            double base = __shfl_up_sync(~0u, upto, 1);
             if (lane == 0)
-                base = PairSum{};
+                base = 0.;
             for (int k = k0; k < k1 && past == segs; ++k) {
-                const PairSum x = part[attempt][k];
-                if (x.positive()) {
+                const double x = part[attempt][k];
+                if (x > 0.) {
                     last = k;
-                    if (base.passes(x, goal))
+                    if (base + x > goal)
                         past = k;
                     else
-                        base.add(x);
+                        base += x;
                 }
             }
             __syncwarp();
             const unsigned over = __ballot_sync(~0u, past < segs), some = __ballot_sync(~0u, last >= 0);
             const int from = over ? __ffs(over) - 1 : (some ? 31 - __clz(some) : 0);
             const int segment = __shfl_sync(~0u, over ? past : last, from);
-            base = shfl(base, from);
+            base = __shfl_sync(~0u, base, from);
             if (lane == 0) {
                 chosen = segment;                     // -1: no weight at all
                 failed = !in;
-                goal_at[0] = over ? goal : PairSum{INFINITY, 0.f};
+                goal_at[0] = over ? goal : INFINITY;
                 goal_at[1] = base;
                 first_over = INT32_MAX;
                 last_positive = -1;
@@ -529,25 +459,25 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
             return;
 
         // ---- that segment again: each thread sums a contiguous run of it
-        const PairSum goal = goal_at[0];
+        const double goal = goal_at[0];
         const int32_t g0 = begin_of(segment), g1 = begin_of(segment + 1);
         const int32_t each = ((a.seg + threads - 1) / threads + 7) / 8 * 8;      // whole words
         const int64_t run0 = static_cast<int64_t>(segment) * a.seg + static_cast<int64_t>(tid) * each - skew;
         const int32_t r0 = static_cast<int32_t>(min(max(run0, static_cast<int64_t>(g0)), static_cast<int64_t>(g1)));
         const int32_t r1 = static_cast<int32_t>(min(max(run0 + each, static_cast<int64_t>(g0)), static_cast<int64_t>(g1)));
-        const PairSum own = w.q ? run_sum<true>(w, r0, r1, skew) : run_sum<false>(w, r0, r1, skew);
-        const PairSum run = warp_upto(own);
+        const double own = w.q ? run_sum<true>(w, r0, r1, skew) : run_sum<false>(w, r0, r1, skew);
+        const double run = warp_upto(own);
         if (lane == 31)
             scan[warp] = run;
         __syncthreads();
-        PairSum at = goal_at[1];                      // the weight before this thread's run
+        double at = goal_at[1];                       // the weight before this thread's run
         for (int k = 0; k < warp; ++k)
-            at.add(scan[k]);
-        const PairSum prior = shfl_up(run, 1);
+            at += scan[k];
+        const double prior = __shfl_up_sync(~0u, run, 1);
         if (lane > 0)
-            at.add(prior);
-        if (own.positive()) {
-            if (at.passes(own, goal))
+            at += prior;
+        if (own > 0.) {
+            if (at + own > goal)
                 atomicMin(&first_over, tid);
             atomicMax(&last_positive, tid);
         }
@@ -557,23 +487,20 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
         if (holder / 32 != warp)
             return;
         const int32_t h0 = __shfl_sync(~0u, r0, holder & 31), h1 = __shfl_sync(~0u, r1, holder & 31);
-        PairSum upto = shfl(at, holder & 31);
+        double upto = __shfl_sync(~0u, at, holder & 31);
         int32_t token = -1;
         for (int32_t v = h0; v < h1; v += 32) {
-            const PairSum x = v + lane < h1 ? w.at(v + lane) : PairSum{};
-            const PairSum sums = warp_upto(x);
-            PairSum before = shfl_up(sums, 1);
-            PairSum from = upto;
-            from.add(lane ? before : PairSum{});
-            const unsigned some = __ballot_sync(~0u, x.positive()),
-                           over = __ballot_sync(~0u, x.positive() && from.passes(x, goal));
+            const double x = v + lane < h1 ? w.any_at(v + lane) : 0.;
+            const double sums = warp_upto(x), before = __shfl_up_sync(~0u, sums, 1);
+            const double from = upto + (lane ? before : 0.);
+            const unsigned some = __ballot_sync(~0u, x > 0.), over = __ballot_sync(~0u, x > 0. && from + x > goal);
             if (over) {
                 token = v + __ffs(over) - 1;
                 break;
             }
             if (some)
                 token = v + 31 - __clz(some);
-            upto.add(shfl(sums, 31));
+            upto += __shfl_sync(~0u, sums, 31);
         }
         if (lane == 0)
             out[A * a.o_pos] = token;

@@ -114,10 +114,12 @@ GDN_API int gdn_token_probs(const gdn_tensor *logits, const gdn_tensor *temperat
  * (GDN_DEV_BAD_SEQLENS; T_i > D + 1 among them) gets num_tokens 0 and -1 in
  * its whole row of out_tokens.  draft_tokens[i, j] = -1 ends a sequence's
  * drafts early: the token is drawn from p_j itself; so does any other token
- * outside the vocabulary, with GDN_DEV_BAD_TOKEN.  Comparisons are exact, sums
- * carry 48 bits or more (W has to stay within the range of fp32).  Where p or p - q is NaN, infinite or not positive it
- * weighs nothing; where that leaves W = 0 after a rejection the token is drawn
- * from p_A, and where that is empty too it is -1, with GDN_DEV_BAD_PROBS.  A u
+ * outside the vocabulary, with GDN_DEV_BAD_TOKEN.  u q < p is compared exactly;
+ * p - q, the sums and u W are fp64, added in an order that the arguments fix
+ * (weights that are multiples of 2^-52 W are summed exactly).  Where p or p - q
+ * is NaN, infinite or not positive it weighs nothing; where that leaves W = 0
+ * after a rejection the token is drawn from p_A, and where that is empty too it
+ * is -1, with GDN_DEV_BAD_PROBS.  A u
  * below 0 counts as 0, one of 1 or more (or NaN) draws the last (first) token
  * of positive weight.  vocab >= 1; N = 0 is GDN_OK with no launch.
  */
