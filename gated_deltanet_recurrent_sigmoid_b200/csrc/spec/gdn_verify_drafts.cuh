@@ -403,7 +403,9 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
             double own = 0.;
             for (int k = k0; k < k1; ++k)
                 own += part[attempt][k];
-            const double upto = warp_upto(own), goal = __shfl_sync(~0u, upto, 31) * u;
+            // (a u of 1 asks for the last token whatever the sums below round to)
+            const double upto = warp_upto(own), whole = __shfl_sync(~0u, upto, 31);
+            const double goal = u < 1.f ? whole * u : INFINITY;
             // the first segment of positive weight past the goal, else the last
             // of positive weight
             int past = segs, last = -1;

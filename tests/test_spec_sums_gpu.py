@@ -85,3 +85,15 @@ def test_half_of_what_a_rejection_leaves(n, shift):
     assert torch.equal(target[::2, 4:4 + 2 * half].double(), p) and torch.equal(draft[:, 0, 4:4 + 2 * half].double(), q)
     tokens = torch.zeros(n, 1, dtype=I32, device="cuda")
     assert bool((drawn(target, draft_tokens=tokens, draft_probs=draft) == 4 + half).all())
+
+
+def test_uniforms_of_one_draw_the_last_token():
+    """u >= 1 counts as the whole weight however its sums round."""
+    n, vocab = 600, 40000
+    g = torch.Generator(device="cuda").manual_seed(7)
+    rows = torch.rand(n, vocab, device="cuda", generator=g) ** 8
+    rows[:, -1] = 1e-12
+    out, num = torch.zeros(n, 1, dtype=I32, device="cuda"), torch.zeros(n, dtype=I32, device="cuda")
+    spec.verify_drafts(rows, torch.zeros(n, 0, dtype=I32, device="cuda"), None, torch.ones(n, 1, device="cuda"), out, num,
+                       cu_seqlens=torch.arange(n + 1, dtype=I32, device="cuda"))
+    assert bool((out == vocab - 1).all())
