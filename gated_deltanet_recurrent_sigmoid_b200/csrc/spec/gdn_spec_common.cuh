@@ -99,6 +99,28 @@ __device__ __forceinline__ bool mbar_wait_peers(unsigned long long *bar, uint32_
     }
 }
 
+// This CTA's own arrival for the next phase of an exchange's mbarrier, which
+// `bytes` of stores from the cluster's CTAs complete.  Copies of the library
+// built for the timeout tests withhold it in the CTAs of one rank, or (-1) in
+// all; product builds define neither switch.
+__device__ __forceinline__ void expect_peers(unsigned long long *bar, uint32_t bytes)
+{
+#ifdef GDN_TEST_WITHHOLD_EXCHANGE
+    if (GDN_TEST_WITHHOLD_EXCHANGE < 0 || cluster_rank() == static_cast<uint32_t>(GDN_TEST_WITHHOLD_EXCHANGE))
+        return;
+#endif
+    sync::mbar_arrive_expect_tx(bar, bytes);
+}
+// The same for a bulk copy into this CTA's shared memory.
+__device__ __forceinline__ void expect_copy(unsigned long long *bar, uint32_t bytes)
+{
+#ifdef GDN_TEST_WITHHOLD_COPY_RANK
+    if (cluster_rank() == GDN_TEST_WITHHOLD_COPY_RANK)
+        return;
+#endif
+    sync::mbar_arrive_expect_state_tx(bar, bytes);
+}
+
 // Address of this CTA's shared variable `p` in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank)
 {

@@ -69,8 +69,9 @@ struct Sum {
 // Over all threads of the cluster, the same bits in each of them (the order is
 // fixed).  Exchanges are numbered: a peer sends its value for number k + 2 only
 // when it has this CTA's for k + 1, which is sent behind the reading of k, so
-// two buffers do.  A wait that gives up leaves sh.failed set, and a value that
-// is the same in the CTA.
+// two buffers do.  A CTA that has given up a wait (sh.failed) sends nothing
+// more, so the cluster's waits run out too and no CTA goes on with values that
+// lack its slice; the result is then the same in the CTA, and not used.
 template <typename Op>
 __device__ __forceinline__ float over_cluster(float x, ProbsShared &sh, uint32_t &number, uint32_t rank, uint32_t size)
 {
@@ -85,14 +86,14 @@ __device__ __forceinline__ float over_cluster(float x, ProbsShared &sh, uint32_t
         sh.warp[warp] = x;
     __syncthreads();
     if (warp == 0) {
+        const bool sends = lane < static_cast<int>(size) && !sh.failed;
         x = lane < static_cast<int>(blockDim.x >> 5) ? sh.warp[lane] : Op::EMPTY;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             x = Op::of(x, __shfl_xor_sync(~0u, x, o));
-        if (lane < static_cast<int>(size))
+        if (sends)
             st_peer(peer_addr(&sh.cta[slot][rank], lane), x, peer_addr(&sh.got[slot], lane));
-        const bool in = mbar_wait_peers(&sh.got[slot], parity);
-        __syncwarp();
+        const bool in = __all_sync(~0u, mbar_wait_peers(&sh.got[slot], parity));
         x = lane < static_cast<int>(size) ? sh.cta[slot][lane] : Op::EMPTY;
 #pragma unroll
         for (int o = PROBS_MAX_CLUSTER / 2; o > 0; o >>= 1)
@@ -100,7 +101,7 @@ __device__ __forceinline__ float over_cluster(float x, ProbsShared &sh, uint32_t
         if (lane == 0) {
             sh.result = x;
             if (in)
-                sync::mbar_arrive_expect_tx(&sh.got[slot], size * sizeof(float));
+                expect_peers(&sh.got[slot], size * sizeof(float));
             else
                 sh.failed = 1;
         }
@@ -148,7 +149,7 @@ struct Slice {
             const uint32_t at = b0 + static_cast<uint32_t>(i) * PROBS_PIECE;
             const uint32_t len = at < b1 ? min(static_cast<uint32_t>(PROBS_PIECE), b1 - at) : 0u;
             if (len) {
-                sync::mbar_arrive_expect_state_tx(&sh.full[i], len);
+                expect_copy(&sh.full[i], len);
                 sync::bulk_load(sh.raw + at, g + at, len, &sh.full[i]);
             } else {
                 sync::mbar_arrive(&sh.full[i]);
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(PROBS_MAX_THREADS, 6) gdn_token_probs_kernel(c
             sync::mbar_init(&sh.full[i], 1);
         for (int i = 0; i < 2; ++i) {
             sync::mbar_init(&sh.got[i], 1);
-            sync::mbar_arrive_expect_tx(&sh.got[i], size * sizeof(float));
+            expect_peers(&sh.got[i], size * sizeof(float));
         }
         sync::fence_barrier_init();
     }

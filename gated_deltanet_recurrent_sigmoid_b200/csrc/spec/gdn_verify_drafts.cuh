@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
         failed = 0;
         for (int k = 0; k < 2; ++k) {
             sync::mbar_init(&got[k], 1);
-            sync::mbar_arrive_expect_tx(&got[k], static_cast<uint32_t>(warps) * size * sizeof(double));
+            expect_peers(&got[k], static_cast<uint32_t>(warps) * size * sizeof(double));
         }
         sync::fence_barrier_init();
     }

@@ -81,7 +81,8 @@ extern "C" {
  * its mass among them.  row_seq[r] = -1 marks a row behind the last sequence:
  * it is not read and its probabilities are left as they were, as are the rows
  * with GDN_DEV_BAD_SEQ; rows with GDN_DEV_BAD_TEMPERATURE become zeros.
- * Exponentials and sums are fp32.  1 <= vocab <= GDN_SPEC_MAX_VOCAB
+ * Exponentials and sums are fp32.  With GDN_DEV_TIMEOUT rows may be missing in
+ * whole or in part; what is written is right.  1 <= vocab <= GDN_SPEC_MAX_VOCAB
  * (GDN_ERR_UNSUPPORTED above); R = 0 is GDN_OK with no launch.
  */
 GDN_API int gdn_token_probs(const gdn_tensor *logits, const gdn_tensor *temperature, const gdn_tensor *row_seq,
