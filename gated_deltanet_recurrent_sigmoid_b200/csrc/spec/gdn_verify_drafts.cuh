@@ -15,10 +15,10 @@
 // fraction of the fp32 rate and still faster than pairs of fp32, 7 operations
 // an element, which keep 36 to 47 bits.
 // Bound by HBM while the rows stream: one row of p, one of q at a rejection.
-// 128 sequences x 131072 fp32, a third of them rejected: 22.7 us (3.9 TB/s; the
+// 128 sequences x 131072 fp32, a third of them rejected: 23.0 us (3.9 TB/s; the
 // 67 MB of p alone stream in 11 us), of which about 2 pass before the rows are
 // known, 4 in the exchange and the second reading, and the rest waits for the
-// sequences that need q too.  One sequence of 32768: 5.3 us of latency.
+// sequences that need q too.  One sequence of 32768: 5.2 us of latency.
 #pragma once
 
 #include "gdn_spec_common.cuh"
@@ -71,7 +71,7 @@ __device__ __forceinline__ double weight(float p, float q, bool in)
 // instruction.  Values that were bf16 by moving the bits of exponent and
 // fraction to their places, which scales by 2^-896 (exactly, subnormals too)
 // and takes two shifts of full rate where the instruction has a quarter of it.
-// 128 x 131072: fp32 22.7 us, by shifts 25.0; bf16 15.6, by instruction 16.7.
+// 128 x 131072: fp32 23.0 us, by shifts 25.0; bf16 15.6, by instruction 16.7.
 template <typename T> struct Wide;
 template <> struct Wide<float> {
     static constexpr double UNIT = 1.;
@@ -236,10 +236,26 @@ __device__ __forceinline__ double lane_sum(const Weights<T> &w, int32_t v0, int3
         if (!__any_sync(~0u, beyond_finite(most, static_cast<const T *>(nullptr))))
             return s;
     }
+    // (eight loads a lane kept ahead of their sums: 128 x 131071 28.0 us against 29.0)
     double s = 0.;
-#pragma unroll 8
-    for (int32_t v = v0 + lane; v < v1; v += 32)
-        s += w.template at<ROW>(v);
+    auto batch = [&](int32_t v, bool whole) {
+        T p[8], q[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const bool in = whole || v + 32 * k < v1;
+            p[k] = in ? w.p[v + 32 * k] : T();           // (zeros weigh nothing)
+            q[k] = ROW && in ? w.q[v + 32 * k] : T();
+        }
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            s += weight<ROW>(Elem<T>::get(p[k]), Elem<T>::get(q[k]), ROW || v + 32 * k != w.out);
+    };
+    int32_t v = v0 + lane;
+    for (; v + 32 * 7 < v1; v += 32 * 8)
+        batch(v, true);
+    if (v < v1)
+        batch(v, false);
     return s;
 }
 
@@ -278,6 +294,7 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
     __shared__ double goal_at[2];                    // u W, and the sum before the chosen segment
     __shared__ unsigned long long got[2];            // the cluster's segment sums are in
     __shared__ int chosen, first_over, last_positive, failed;
+    __shared__ float uniform;                        // u, not below 0
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_index(), threads = blockDim.x, warps = threads >> 5;
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int32_t i = static_cast<int32_t>(blockIdx.x / size);
@@ -298,7 +315,8 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
     const float *const uniforms = a.uniforms + i * a.u_seq;
     int32_t x_first = lane < a.D ? tokens[lane * a.x_pos] : 0;
     float u_first = lane < a.D ? uniforms[lane * a.u_pos] : 0.f;
-    const float u = fmaxf(uniforms[a.D * a.u_pos], 0.f);              // NaN: 0
+    if (tid == 0)
+        uniform = fmaxf(uniforms[a.D * a.u_pos], 0.f);                // NaN: 0
     int32_t start, len;
     bool runs = rows_of(a.cu_seqlens, a.T_fixed, a.T_tot, i, &start, &len);
     if (!runs || len - 1 > a.D) {
@@ -354,13 +372,19 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
                 report(a.status, GDN_DEV_BAD_TOKEN);
         }
     }
-    if (rank == 0) {
+    if (rank == 0)
         for (int j = tid; j <= a.D; j += threads)
             if (j != A)
                 out[j * a.o_pos] = j < A ? tokens[j * a.x_pos] : -1;
-        if (tid == 0)
-            a.num[i * a.n_seq] = A + 1;
-    }
+    // num_tokens is written together with the token, by the CTA that has it, so
+    // a count never stands beside a token that was not drawn.  (The sequence's
+    // number is derived again and u waits in shared memory: kept in registers
+    // over the sums they made others spill, 128 x 131072 fp32 23.1 -> 23.8 us.)
+    auto finish = [&](int32_t token) {
+        const int32_t seq = static_cast<int32_t>(blockIdx.x / cluster_size());
+        a.out[seq * a.o_seq + A * a.o_pos] = token;
+        a.num[seq * a.n_seq] = A + 1;
+    };
 
     // ---- the sum of each segment
     Weights<T> w = {target + A * a.t_row, less == Less::row ? draft + A * a.d_pos : nullptr,
@@ -397,14 +421,14 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
         // ---- where the running sum passes u W: each lane of the first warp
         // takes a run of `per` segments
         if (warp == 0) {
-            const bool in = mbar_wait_peers(&got[attempt], 0);
-            __syncwarp();
+            const bool in = __all_sync(~0u, mbar_wait_peers(&got[attempt], 0));
             const int per = (segs + 31) / 32, k0 = lane * per, k1 = min(k0 + per, segs);
             double own = 0.;
             for (int k = k0; k < k1; ++k)
                 own += part[attempt][k];
             // (a u of 1 asks for the last token whatever the sums below round to)
             const double upto = warp_upto(own), whole = __shfl_sync(~0u, upto, 31);
+            const float u = uniform;
             const double goal = u < 1.f ? whole * u : INFINITY;
             // the first segment of positive weight past the goal, else the last
             // of positive weight
@@ -437,8 +461,8 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
             }
         }
         if (__syncthreads_or(failed)) {
-            if (rank == 0 && tid == 0) {
-                out[A * a.o_pos] = -1;
+            if (tid == 0) {                           // (the CTA that finds the token may not have given up)
+                a.num[static_cast<int32_t>(blockIdx.x / cluster_size()) * a.n_seq] = 0;
                 report(a.status, GDN_DEV_TIMEOUT);
             }
             cluster_leave();
@@ -452,7 +476,7 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
                 continue;
             }
             if (rank == 0 && tid == 0) {
-                out[A * a.o_pos] = -1;
+                finish(-1);
                 report(a.status, GDN_DEV_BAD_PROBS);
             }
             return;
@@ -505,7 +529,7 @@ __global__ void __launch_bounds__(VERIFY_MAX_THREADS, 4) gdn_verify_drafts_kerne
             upto += __shfl_sync(~0u, sums, 31);
         }
         if (lane == 0)
-            out[A * a.o_pos] = token;
+            finish(token);
         return;
     }
 }

@@ -122,7 +122,9 @@ GDN_API int gdn_token_probs(const gdn_tensor *logits, const gdn_tensor *temperat
  * after a rejection the token is drawn from p_A, and where that is empty too it
  * is -1, with GDN_DEV_BAD_PROBS.  A u
  * below 0 counts as 0, one of 1 or more (or NaN) draws the last (first) token
- * of positive weight.  vocab >= 1; N = 0 is GDN_OK with no launch.
+ * of positive weight.  With GDN_DEV_TIMEOUT a sequence may have num_tokens 0 and
+ * an out_tokens row that is not to be read; counts other than 0 stand beside the
+ * whole answer.  vocab >= 1; N = 0 is GDN_OK with no launch.
  */
 GDN_API int gdn_verify_drafts(const gdn_tensor *target_probs, const gdn_tensor *draft_tokens,
                               const gdn_tensor *draft_probs, const gdn_tensor *uniforms,
