@@ -80,6 +80,15 @@ int check_vector(const gdn_tensor *t, int64_t n, int32_t dtype = GDN_DTYPE_I32)
 // Rows of a written matrix must not run into each other.
 bool rows_apart(const gdn_tensor *t) { return t->shape[0] <= 1 || t->stride[0] >= t->shape[1]; }
 
+// Whether runs of `unit` elements that begin at i * s0 + j * s1 (i < n0, j < n1)
+// lie apart: either index's entries inside one step of the other's.
+bool items_apart(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t unit)
+{
+    if ((n0 > 1 && s0 < unit) || (n1 > 1 && s1 < unit))
+        return false;
+    return n0 <= 1 || n1 <= 1 || s0 >= (n1 - 1) * s1 + unit || s1 >= (n0 - 1) * s0 + unit;
+}
+
 cudaStream_t stream_of(const gdn_extra *x) { return x ? static_cast<cudaStream_t>(x->stream) : nullptr; }
 uint32_t *status_of(const gdn_extra *x) { return x ? x->device_status : nullptr; }
 
@@ -293,9 +302,7 @@ GDN_API int gdn_verify_drafts(const gdn_tensor *target_probs, const gdn_tensor *
     if (vocab > 1 && (target_probs->stride[target_probs->ndim - 1] != 1 || (draft_probs && draft_probs->stride[2] != 1)))
         return GDN_ERR_SHAPE;
     // written entries must not share an address
-    if (!((out_tokens->stride[1] >= 1 || D == 0) && (N <= 1 || out_tokens->stride[0] > D * out_tokens->stride[1] ||
-                                                      (out_tokens->stride[0] >= 1 && out_tokens->stride[1] > (N - 1) * out_tokens->stride[0]))) ||
-        (N > 1 && num_tokens->stride[0] < 1))
+    if (!items_apart(N, out_tokens->stride[0], D + 1, out_tokens->stride[1], 1) || (N > 1 && num_tokens->stride[0] < 1))
         return GDN_ERR_SHAPE;
     for (const gdn_tensor *t : {target_probs, draft_tokens, draft_probs, uniforms, out_tokens, num_tokens})
         if (t && !aligned(t->data, elem_size(t->dtype)))
@@ -378,7 +385,7 @@ GDN_API int gdn_commit_states(const gdn_tensor *intermediate_states, const gdn_t
             return GDN_ERR_ALIGN;
     }
     // states of the pool must not share addresses
-    if ((HV > 1 && pool->stride[1] < kState * kState) || (slots > 1 && pool->stride[0] < kState * kState))
+    if (!items_apart(slots, pool->stride[0], HV, pool->stride[1], kState * kState))
         return GDN_ERR_SHAPE;
     GDN_TRY(check_alias({pool}, {in, num_tokens, state_indices, cu_seqlens}, extra));
     if (N * HV > INT32_MAX / gdn::spec::COMMIT_PIECES)

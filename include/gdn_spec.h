@@ -145,7 +145,9 @@ GDN_API int gdn_verify_drafts(const gdn_tensor *target_probs, const gdn_tensor *
  *   state_indices        int32  [N]               contiguous
  *   cu_seqlens           int32  [N + 1] or NULL   contiguous; NULL = T_tot / N
  *                                                 tokens each
- * States are K = V = 128 with the layout rules of gdn_decode.h.  The
+ * States are K = V = 128 with the layout rules of gdn_decode.h; those of the
+ * pool share no address, slots inside one head stride or heads inside one slot
+ * stride (GDN_ERR_SHAPE).  The
  * non-negative state_indices must be distinct.  A sequence with a bad slot,
  * bad cu_seqlens or a count outside 0 .. T_i (GDN_DEV_BAD_SLOT,
  * GDN_DEV_BAD_SEQLENS, GDN_DEV_BAD_COUNT) is skipped.  N = 0 or T_tot = 0 is
