@@ -15,7 +15,8 @@ kernels, each call launches one, on ``stream`` or else on the stream that is
 current when the call is made, on the tensors' device.  A non-zero status
 raises ``binding.GdnError``; tensors that are not on one CUDA device raise
 ValueError.  The ``Prepared*`` classes keep the descriptors of a call that is
-made again and again on the same buffers, which must stay alive.
+made again and again on the same buffers, which must stay alive; several
+threads may use one object, each on its own current stream.
 """
 from __future__ import annotations
 
@@ -53,6 +54,7 @@ class GdnStepMapsCall(ctypes.Structure):
 
 
 _LIB = None
+_STREAMS_KEPT = 64       # streams that a prepared call remembers its arguments for
 
 
 def library_path() -> str:
@@ -113,8 +115,9 @@ class _Prepared:
         if stream is not None and stream.device_index != self._device:
             raise ValueError("the stream is not one of the tensors' device")
 
-    def _bind(self, more_flags: int = 0):
-        """(function, arguments) with ``more_flags`` beside the call's own."""
+    def _bind(self, more_flags: int = 0, extra: Optional[GdnExtra] = None):
+        """(function, arguments) with ``more_flags`` beside the call's own, and
+        ``extra`` in the place of the object's."""
         raise NotImplementedError
 
     @staticmethod
@@ -125,23 +128,34 @@ class _Prepared:
             raise GdnError(status, status_string(status))
 
     def _ready(self) -> None:
-        fn, args = self._bind()
-        self._bound = args
+        fn, _ = self._bind()
         self._fn = getattr(load().untyped, fn.__name__)
-        self._args = tuple(ctypes.c_void_p(ctypes.addressof(a._obj)) if hasattr(a, "_obj") else a for a in args)
-        self._stream = None
+        self._by_stream = {}
+        self._args = None if self._follow else self._for_stream(self._extra.stream)
+
+    def _for_stream(self, stream: int):
+        """The arguments on ``stream`` (pointers, and what they point at).  They
+        are never written again: the library runs without the interpreter's
+        lock, so another thread may be inside a call with its own."""
+        extra = GdnExtra.from_buffer_copy(self._extra)
+        extra.stream = stream
+        _, args = self._bind(extra=extra)
+        return tuple(ctypes.c_void_p(ctypes.addressof(a._obj)) if hasattr(a, "_obj") else a for a in args), args
 
     def __call__(self) -> None:
-        device = self._device
-        if self._follow:
+        device, bound = self._device, self._args
+        if bound is None:
             stream = torch._C._cuda_getCurrentRawStream(device)
-            if stream != self._stream:
-                self._extra.stream = self._stream = stream
+            bound = self._by_stream.get(stream)
+            if bound is None:
+                if len(self._by_stream) >= _STREAMS_KEPT:
+                    self._by_stream = {}
+                bound = self._by_stream[stream] = self._for_stream(stream)
         if torch._C._cuda_getDevice() == device:
-            status = self._fn(*self._args)
+            status = self._fn(*bound[0])
         else:
             with torch.cuda.device(device):
-                status = self._fn(*self._args)
+                status = self._fn(*bound[0])
         if status != OK:
             raise GdnError(status, status_string(status))
 
@@ -167,9 +181,9 @@ class PreparedTokenProbs(_Prepared):
         super().__init__((logits, temperature, row_seq, probs), device_status, stream)
         self._ready()
 
-    def _bind(self, more_flags: int = 0):
+    def _bind(self, more_flags: int = 0, extra: Optional[GdnExtra] = None):
         return load().gdn_token_probs, (*self._refs(), ctypes.c_uint32(self._flags | more_flags),
-                                        ctypes.byref(self._extra))
+                                        ctypes.byref(extra or self._extra))
 
 
 class PreparedVerifyDrafts(_Prepared):
@@ -182,9 +196,9 @@ class PreparedVerifyDrafts(_Prepared):
                           num_tokens), device_status, stream)
         self._ready()
 
-    def _bind(self, more_flags: int = 0):
+    def _bind(self, more_flags: int = 0, extra: Optional[GdnExtra] = None):
         return load().gdn_verify_drafts, (*self._refs(), ctypes.c_uint32(self._flags | more_flags),
-                                          ctypes.byref(self._extra))
+                                          ctypes.byref(extra or self._extra))
 
 
 class PreparedCommitStates(_Prepared):
@@ -197,9 +211,9 @@ class PreparedCommitStates(_Prepared):
                          stream)
         self._ready()
 
-    def _bind(self, more_flags: int = 0):
+    def _bind(self, more_flags: int = 0, extra: Optional[GdnExtra] = None):
         return load().gdn_commit_states, (*self._refs(), ctypes.c_uint32(self._flags | more_flags),
-                                          ctypes.byref(self._extra))
+                                          ctypes.byref(extra or self._extra))
 
 
 class PreparedStepMaps(_Prepared):
@@ -214,14 +228,14 @@ class PreparedStepMaps(_Prepared):
                          device_status, stream)
         self._ready()
 
-    def _bind(self, more_flags: int = 0):
+    def _bind(self, more_flags: int = 0, extra: Optional[GdnExtra] = None):
         call = GdnStepMapsCall()
         for name, d in zip(_MAPS_TENSORS, self._descs):
             if d is not None:
                 setattr(call, name, ctypes.pointer(d))
         call.block_size = self._block_size
         call.flags = self._flags | more_flags
-        call.extra = ctypes.pointer(self._extra)
+        call.extra = ctypes.pointer(extra or self._extra)
         return load().gdn_step_maps, (ctypes.byref(call),)
 
 
