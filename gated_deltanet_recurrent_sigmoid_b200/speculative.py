@@ -166,8 +166,7 @@ class _Prepared:
         """Call now, for tensors that the caller may free right after it."""
         self()
         tensors, status, stream = self._keep
-        if stream is not None and stream.cuda_stream != torch._C._cuda_getCurrentRawStream(self._device) \
-                and not torch.cuda.is_current_stream_capturing():
+        if stream is not None and stream.cuda_stream != torch._C._cuda_getCurrentRawStream(self._device):
             for t in (*tensors, status):
                 if t is not None:
                     t.record_stream(stream)
