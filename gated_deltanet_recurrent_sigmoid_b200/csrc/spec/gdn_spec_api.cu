@@ -423,6 +423,8 @@ GDN_API int gdn_step_maps(const gdn_step_maps_call *c)
     GDN_TRY(check_call(c->flags, c->extra));
     GDN_TRY(check_vector(c->lengths, -1));
     const int64_t N = c->lengths->shape[0];
+    if (N > INT32_MAX - 4 * gdn::spec::MAPS_THREADS)       // requests are counted in 32 bits, so many at a time
+        return GDN_ERR_SHAPE;
     GDN_TRY(check_vector(c->context, N));
     GDN_TRY(check_vector(c->slots, N));
     GDN_TRY(check_vector(c->cu_seqlens, N + 1));

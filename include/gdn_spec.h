@@ -188,7 +188,8 @@ GDN_API int gdn_commit_states(const gdn_tensor *intermediate_states, const gdn_t
  * GDN_DEV_BAD_BLOCKS) or slot < -1 (GDN_DEV_BAD_SLOT) does not run.  Where the
  * C rows or the free blocks run out, the first request that does not fit and
  * every later one do not run (GDN_DEV_NO_ROOM); what does not run takes no
- * block.  Launched even with N = 0 (cu_seqlens = {0}, the rest -1).
+ * block.  Launched even with N = 0 (cu_seqlens = {0}, the rest -1); N is at most
+ * INT32_MAX - 1024.
  */
 typedef struct gdn_step_maps_call {
     const gdn_tensor *lengths, *context, *slots;

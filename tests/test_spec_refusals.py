@@ -48,3 +48,24 @@ def test_commit_takes_pools_whose_states_lie_apart(slots, heads, slot, head):
 def test_verify_refuses_outputs_that_share_addresses(n, d, strides):
     out = torch.zeros(32, dtype=I32).as_strided((n, d + 1), strides)
     refused(binding.ERR_SHAPE, lambda: make_verify(N=n, D=d), out_tokens=out)
+
+
+def far_vector(n, place, dtype=3):
+    """A descriptor of n entries at an address of its own; nothing reads it."""
+    d = binding.GdnTensor()
+    d.data, d.dtype, d.ndim = (place + 1) << 40, dtype, 1
+    d.shape[0], d.stride[0] = n, 1
+    return d
+
+
+@pytest.mark.parametrize("n,status", [(2**31 - 2, binding.ERR_SHAPE), (2**31 - 1024, binding.ERR_SHAPE),
+                                      (2**31 - 1025, binding.OK), (2**30, binding.OK), (0, binding.OK)])
+def test_maps_refuses_more_requests_than_its_counters_hold(n, status):
+    """The kernel counts requests in 32 bits, 1024 at a time."""
+    call = spec.GdnStepMapsCall()
+    names = ("lengths", "context", "slots", "cu_seqlens", "state_indices", "row_seq", "positions")
+    descs = [far_vector(n + 1 if k == "cu_seqlens" else 64 if k in ("row_seq", "positions") else n, i) for i, k in enumerate(names)]
+    for k, d in zip(names, descs):
+        setattr(call, k, ctypes.pointer(d))
+    call.flags = spec.CHECK_ONLY
+    assert spec.load().gdn_step_maps(ctypes.byref(call)) == status
