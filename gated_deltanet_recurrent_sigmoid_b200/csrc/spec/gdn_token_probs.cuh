@@ -111,12 +111,13 @@ __device__ __forceinline__ float over_cluster(float x, ProbsShared &sh, uint32_t
 }
 
 // 2^((x - m) c) up to a factor that is the same for the whole row.  fast:
-// one fused multiply-add, x c - (m c), the rounding of m c being that factor;
-// careful: any maximum and temperature, NaN as 0.
+// one fused multiply-add, x c - by, by = m c, whose rounding is that factor.
+// careful: any maximum and temperature, NaN as 0; the difference times `by`,
+// which is 1, or 2^64 beside a c that is smaller by as much.
 struct Power {
-    float c, top, mc;
-    __device__ float fast(float x) const { return ex2(fmaf(x, c, -mc)); }
-    __device__ float careful(float x) const { return x == top ? 1.f : (x == x ? ex2((x - top) * c) : 0.f); }
+    float c, top, by;
+    __device__ float fast(float x) const { return ex2(fmaf(x, c, -by)); }
+    __device__ float careful(float x) const { return x == top ? 1.f : (x == x ? ex2((x - top) * by * c) : 0.f); }
 };
 
 // This CTA's slice of one row, in shared memory from el[0] on: the 16-byte
@@ -273,10 +274,10 @@ __global__ void __launch_bounds__(PROBS_MAX_THREADS, 6) gdn_token_probs_kernel(c
             const bool bad = !(t >= 0.f) || isinf(t), greedy = t == 0.f;
             if (bad && rank == 0 && tid == 0)
                 report(p.status, GDN_DEV_BAD_TEMPERATURE);
-            // log2(e) / t, at most 1e38 so that 0 * c is 0
-            const float c = greedy || bad ? 0.f : fminf(1.44269504f / t, 1e38f);
-            const Power power = {c, top, top * c};
-            bool fast = !greedy && !bad && fabsf(power.mc) < 1048576.f;
+            // log2(e) / t, infinite for t < 4.3e-39: m c is not within 2^20 then
+            const float c = greedy || bad ? 0.f : 1.44269504f / t;
+            Power power = {c, top, top * c};
+            bool fast = !greedy && !bad && fabsf(power.by) < 1048576.f;
             const bool zeros = bad || top == -INFINITY;
             float inv = 0.f;
             int32_t pick = -1;
@@ -309,6 +310,9 @@ __global__ void __launch_bounds__(PROBS_MAX_THREADS, 6) gdn_token_probs_kernel(c
                     inv = 1.f / s;
                 }
                 if (!fast) {
+                    const bool tiny = isinf(c);
+                    power.by = tiny ? 0x1p64f : 1.f;
+                    power.c = tiny ? 1.44269504f / (t * 0x1p64f) : c;
                     float s = 0.f;
                     for (int32_t j = tid; j < sl.n; j += threads)
                         s += power.careful(Elem<TIn>::get(sl.el[j]));
