@@ -163,24 +163,27 @@ cudaError_t launch_probs(const gdn::spec::ProbsParams &p, int64_t rows, int clus
 }
 
 // CTAs per row of token probabilities: slices of at most 16 KB as far as 8 CTAs
-// give them, and more CTAs while the grid leaves SMs idle and a slice keeps
-// 1024 elements.  Measured for 512 rows bf16 -> fp32: 4096 logits in 1 CTA 5.8
-// us, in 4 8.5; 32768 in 1 28.8, in 4 22.0, in 8 25.2; 50021 fp32 in 4 43.5, in
-// 8 41.0.  16 CTAs where 8 would leave a slice over 32 KB, or SMs idle (131072
-// fp32 in 8 94 us, in 16 91; bf16 in 8 69, in 16 72; one row of it in 8 5.3, in
-// 16 4.4).
+// give them, and more CTAs while the grid leaves SMs idle and a slice keeps 512
+// elements.  Measured for 512 rows bf16 -> fp32: 4096 logits in 1 CTA 5.8 us, in
+// 4 8.5; 32768 in 1 28.8, in 4 22.0, in 8 25.2; 50021 fp32 in 4 43.5, in 8 41.0.
+// 16 CTAs where 8 would leave a slice over 55 KB, of which an SM holds fewer than
+// four, or SMs idle.  512 rows in 8 and in 16, fp32: 66000 logits 45.8 us and
+// 65.0, 110000 74.8 and 81.9, 114688 87.1 and 84.0, 131072 94.4 and 91.5; bf16
+// -> fp32: 140000 77.9 and 89.7, 225000 120.2 and 125.5, 229376 128.4 and 126.9;
+// one row of 131072 bf16 5.3 and 4.4.  (40 rows of bf16, 131072 to 220000, are 5
+// to 8 % faster in 16, of fp32 up to 8 % slower.)
 int probs_cluster(int64_t rows, int64_t row_bytes, int64_t vocab, int sms)
 {
     int c = 1;
     while (c < 8 && (row_bytes > c * 16384ll || (rows * c < sms && vocab > c * 1024ll)))
         c *= 2;
-    if (c == 8 && (row_bytes > 8 * 32768ll || (rows * 16 <= sms && vocab > 16 * 1024ll)))
+    if (c == 8 && (row_bytes > 8 * 56320ll || (rows * 16 <= sms && vocab > 16 * 1024ll)))
         c = 16;
     return c;
 }
 
 // CTAs per sequence of a verification: as many (up to 8) as stay resident at
-// once, eight of 128 threads an SM, while a CTA keeps 1024 elements.
+// once, eight of 128 threads an SM, while a CTA keeps 512 elements.
 int verify_cluster(int64_t sequences, int64_t vocab, int sms)
 {
     int c = 1;

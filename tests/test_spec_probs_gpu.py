@@ -61,6 +61,14 @@ def test_probabilities_within_their_rounding(rows, vocab, dtype, out):
     check(x, t, out)
 
 
+# either side of where rows go from 8 CTAs to 16
+@pytest.mark.parametrize("dtype,vocab", [(F32, 66001), (F32, 112639), (F32, 112641), (BF16, 140001), (BF16, 225279), (BF16, 225283)])
+def test_rows_about_the_limit_of_sixteen(dtype, vocab):
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    x = (torch.randn(70, vocab, device="cuda", generator=g) * 4).to(dtype)
+    check(x, torch.rand(70, device="cuda", generator=g) + 0.3, F32)
+
+
 # from the smallest number, through c = log2(e) / t out of range, to where it fits
 @pytest.mark.parametrize("t", [1e-45, 1e-44, 1e-42, 1e-40, 3e-39, 4.3e-39, 1e-38, 1.2e-38, 1.44e-38, 1e-37, 1e-30])
 @pytest.mark.parametrize("base", [0.0, 1.0])
