@@ -143,7 +143,8 @@ cudaError_t launch_probs(const gdn::spec::ProbsParams &p, int64_t rows, int clus
     // The clusters that fit the GPU at once, for the last launch shape asked
     // for on each device: shape in the upper half, clusters in the lower.
     static std::atomic<uint64_t> resident[PerDevice::kMaxDevices];
-    const uint64_t shape = static_cast<uint64_t>(smem) << 10 | static_cast<uint64_t>(cluster) << 6 | threads / 32;
+    // (18 bits of shared memory, 5 of the cluster, 6 of the warps)
+    const uint64_t shape = static_cast<uint64_t>(smem) << 11 | static_cast<uint64_t>(cluster) << 6 | threads / 32;
     uint64_t known = err == cudaSuccess ? resident[dev].load(std::memory_order_relaxed) : 0;
     if (err == cudaSuccess && known >> 32 != shape) {
         int clusters = 0;
