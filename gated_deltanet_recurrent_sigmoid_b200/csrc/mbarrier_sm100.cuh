@@ -45,12 +45,13 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(unsigned long long *bar, u
 
 // The expect-tx arrival paired with a kernel's first bulk copy of a
 // sequence's data -- its state, or the first piece's record for a kernel that
-// loads the state with plain loads (the barrier phase completes when this
-// arrival and the copy's bytes are both in).  The test copy of the library (tests/timeout_probe/) is compiled with
-// GDN_TEST_WITHHOLD_STATE_ARRIVAL, which drops the arrival: the copy still
-// lands, its phase never completes, and the kernel's bounded wait for it runs
-// out -- how the timeout paths are made to fire on a GPU without a fault.
-// Product builds never define it.
+// loads the state with plain loads -- and with every piece of a logit row in
+// the probabilities' kernel (the barrier phase completes when this arrival and
+// the copy's bytes are both in).  The test copies of the libraries
+// (tests/timeout_probe/) are compiled with GDN_TEST_WITHHOLD_STATE_ARRIVAL,
+// which drops the arrival: the copy still lands, its phase never completes, and
+// the kernel's bounded wait for it runs out -- how the timeout paths are made
+// to fire on a GPU without a fault.  Product builds never define it.
 __device__ __forceinline__ void mbar_arrive_expect_state_tx(unsigned long long *bar, uint32_t bytes)
 {
 #ifdef GDN_TEST_WITHHOLD_STATE_ARRIVAL

@@ -10,11 +10,12 @@
 // distributed shared memory.  What a row needs besides its logits is loaded a
 // row ahead.
 // Bound by HBM: each logit read once, each probability written once.  512 x
-// 131072 bf16 -> fp32 in 70 us, 5.8 TB/s, 0.89 of the measured copy rate; fp32
-// -> fp32 in 91 us (0.91); bf16 -> bf16 in 57 us (0.72: the two powers a logit
-// and the issue slots begin to count).  A single row of
-// 32768 takes 3.7 us, all of it latency.  CTAs of 512 threads, fewer of them
-// resident, took 84 us; one pass with a running maximum and sum 116.
+// 131072 bf16 -> fp32 in 69 us, 5.8 TB/s, 0.90 of the measured copy rate; fp32
+// -> fp32 in 92 us (0.90); fp32 -> bf16 in 85 us (0.73) and bf16 -> bf16 in 59
+// us (0.71: the two powers a logit and the issue slots begin to count).  A
+// single row of 32768 takes 3.6 us, all of it latency.  CTAs of 512 threads,
+// fewer of them resident, took 84 us; one pass with a running maximum and sum
+// 116.
 #pragma once
 
 #include "gdn_spec_common.cuh"
@@ -37,8 +38,8 @@ struct ProbsParams {
 
 constexpr int PROBS_MAX_THREADS = 256;
 // Bytes per bulk copy and mbarrier.  (8 KB pieces, whose maxima overlap the
-// copies of the later ones: 1 % slower throughout, one row of 131072 5.5 us
-// against 5.2.)
+// copies of the later ones: up to 2 % slower, 512 x 131072 fp32 93.6 us against
+// 92.0, one row of 131072 4.5 against 4.4.)
 constexpr int PROBS_PIECE = 32768;
 constexpr int PROBS_MAX_CLUSTER = 16;
 constexpr int PROBS_MAX_SLICE_BYTES = GDN_SPEC_MAX_VOCAB / PROBS_MAX_CLUSTER * 4;

@@ -20,7 +20,8 @@
  * the caller owns all memory, every argument check happens on the host before
  * anything is enqueued, a call launches one kernel on extra->stream, allocates
  * nothing, keeps nothing and can be captured in a CUDA graph.  No written
- * tensor may overlap any other tensor of the call (GDN_ERR_ALIAS).  In
+ * tensor may overlap any other tensor of the call (GDN_ERR_ALIAS; the address
+ * ranges are compared, so interleaved views count as overlapping).  In
  * `extra` only stream and device_status are used; every other field must be 0
  * (GDN_ERR_ARG).  flags: GDN_SPEC_CHECK_ONLY, and GDN_LAUNCH_PDL, which every
  * call here implies (the kernel may be scheduled while the previous one on the
@@ -120,8 +121,8 @@ GDN_API int gdn_token_probs(const gdn_tensor *logits, const gdn_tensor *temperat
  * (weights that are multiples of 2^-52 W are summed exactly).  Where p or p - q
  * is NaN, infinite or not positive it weighs nothing; where that leaves W = 0
  * after a rejection the token is drawn from p_A, and where that is empty too it
- * is -1, with GDN_DEV_BAD_PROBS.  A u
- * below 0 counts as 0, one of 1 or more (or NaN) draws the last (first) token
+ * is -1, with GDN_DEV_BAD_PROBS.  The draw's u counts as 0 when it is below 0,
+ * one of 1 or more (or NaN) draws the last (first) token
  * of positive weight.  With GDN_DEV_TIMEOUT a sequence may have num_tokens 0 and
  * an out_tokens row that is not to be read; counts other than 0 stand beside the
  * whole answer.  vocab >= 1; N = 0 is GDN_OK with no launch.
